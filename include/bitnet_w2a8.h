@@ -395,10 +395,11 @@ bitnet_status bitnet_w2a8_gemm_acc(const bitnet_weight *w, const int8_t *q_dev,
  * Index arrays (cu_tokens, cache_len, seq_len, block_table) are int32 device
  * memory, 4-byte aligned, read by the kernels, so one captured graph serves
  * every step.  A page id outside 0 .. num_pages-1, a length that needs more
- * pages than a table row has, or sequence bounds that decrease or pass the
- * token count are met by the kernels' own checks: nothing is read or written
- * through them and BITNET_ERR_VALUE is latched (the rows concerned are then
- * unspecified).  Table entries behind a sequence's last page are not read.
+ * pages than a table row has, a negative cache_len, or sequence bounds that
+ * decrease, begin below 0 or pass the token count (of any sequence, with or
+ * without tokens) are met by the kernels' own checks: nothing is read or
+ * written through them and BITNET_ERR_VALUE is latched (the rows concerned are
+ * then unspecified).  Table entries behind a sequence's last page are not read.
  * Lengths may be zero.
  * ---------------------------------------------------------------------- */
 

@@ -100,6 +100,15 @@ __device__ __forceinline__ void store_from_f32(T *p, const float (&v)[N]) {
     }
 }
 
+// Latches BOUNDS if sequence i's rows go backwards, begin before row 0 or pass
+// `rows`, or its length in the cache (`len`, if given) is negative.  Done for every
+// sequence apart from the work units below: one behind the last row, or one that
+// goes backwards, may own no unit.
+__device__ __forceinline__ void check_sequence(const int32_t *cu, int64_t rows, const int32_t *len, int64_t i, unsigned *err) {
+    const int lo = cu[i], hi = cu[i + 1];
+    if (lo < 0 || hi < lo || hi > rows || (len && len[i] < 0)) atomicOr(err, kErrBounds);
+}
+
 // Sequences of a packed batch own consecutive work units: sequence i those from
 // base(i) = cu[i] / per + slack * i on (per: tokens of a unit; slack: units that
 // a sequence may need beyond tokens / per).  The bases need no pass over the

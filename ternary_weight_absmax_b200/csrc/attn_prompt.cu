@@ -17,6 +17,7 @@
 //                   slots half a step apart: with an issuer for each slot both
 //                   softmaxes ran at the same time, then both slots' MMAs
 //                   (566 us on 8192 tokens and 32 heads of 128).
+//   warps 10, 11    check the bounds of 32 sequences, then idle.
 // Tensor memory: S0 | S1 | O0 | O1.
 //
 // The running maximum is only a reference: a row keeps it while its scores
@@ -52,7 +53,7 @@ namespace {
 
 constexpr int kTile = 128;  // queries of a slot
 constexpr int kSlots = 2;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kIdleWarp = 10;
 constexpr int kThreads = 384;  // three warpgroups: two softmax, one for loads and MMAs
 constexpr int kParts = 2;      // the weights of a tile are handed to the MMA in two parts
 constexpr uint32_t kDrainLimit = 1u << 22;
@@ -219,6 +220,12 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+    if (warp >= kIdleWarp) {  // 32 sequences a CTA: there are more CTAs than sequences
+        const int64_t i = (int64_t)blockIdx.x * 32 + lane;
+        const bool of_q = warp == kIdleWarp;
+        if (i < a.seqs) check_sequence(of_q ? a.cu_q : a.cu_k, of_q ? a.q_tokens : a.k_tokens, nullptr, i, a.err);
+    }
+
     // The work: kv head, sequence, two neighbours of the list (row tile, head
     // of the group), the last rows (the longest walks) first.
     const int kvh = blockIdx.x % a.kv_heads;
@@ -226,10 +233,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const int64_t unit = rest / a.pairs_per_tile;
     const int seq = find_seq(a.cu_q, a.seqs, unit, kTile, 1);
     const int64_t q0 = a.cu_q[seq], q1 = a.cu_q[seq + 1], k0 = a.cu_k[seq], k1 = a.cu_k[seq + 1];
-    if (q0 < 0 || q1 < q0 || q1 > a.q_tokens || k0 < 0 || k1 < k0 || k1 > a.k_tokens) {
-        if (threadIdx.x == 0) atomicOr(a.err, kErrBounds);
-        return;
-    }
+    if (q0 < 0 || q1 < q0 || q1 > a.q_tokens || k0 < 0 || k1 < k0 || k1 > a.k_tokens) return;  // latched by check_sequence
     const int lq = (int)(q1 - q0), lk = (int)(k1 - k0);
     const int64_t local = unit - unit_base(a.cu_q, seq, kTile, 1);
     const int64_t items = (int64_t)((lq + kTile - 1) / kTile) * a.group;

@@ -189,6 +189,11 @@ kv_append_kernel(const AppendArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == kWarps - 1 && blockIdx.y == 0) {
+#pragma unroll 1
+        for (int64_t i = (int64_t)blockIdx.x * 32 + lane; i < a.seqs; i += (int64_t)gridDim.x * 32)
+            check_sequence(a.cu, a.tokens, a.cache_len, i, a.err);
+    }
     // Warp 0 finds the block: its positions, their rows, and its page.
     __shared__ struct {
         int64_t first, tok;  // position and row of the first new token
@@ -204,7 +209,7 @@ kv_append_kernel(const AppendArgs a) {
         if (seq < 0) seq = find_seq(a.cu, a.seqs, unit, a.per, a.slack);
         const int64_t t0 = a.cu[seq], t1 = a.cu[seq + 1];
         const int64_t old = a.cache_len[seq];
-        const bool bad = t0 < 0 || t1 < t0 || t1 > a.tokens || old < 0;
+        const bool bad = t0 < 0 || t1 < t0 || t1 > a.tokens || old < 0;  // latched by check_sequence
         const int64_t blk = old / kKvBlock + (unit - unit_base(a.cu, seq, a.per, a.slack));  // block of the sequence
         const int64_t first = max(old, blk * kKvBlock);
         const int64_t last = min(old + (t1 - t0), (blk + 1) * kKvBlock);
@@ -214,7 +219,7 @@ kv_append_kernel(const AppendArgs a) {
         if (n > 0 && pg < a.max_pages) page = a.table[(int64_t)seq * a.max_pages + pg];
         if (page >= a.c.num_pages) page = -1;
         if (lane == 0) {
-            if (bad || (n > 0 && (page < 0 || (a.rope && last > a.rope_rows)))) atomicOr(a.err, kErrBounds);
+            if (n > 0 && (page < 0 || (a.rope && last > a.rope_rows))) atomicOr(a.err, kErrBounds);
             b.first = first, b.tok = t0 + (first - old);
             b.n = n, b.slot = (int)(first - blk * kKvBlock), b.page = page < 0 ? -1 : (int)page;
         }
@@ -382,12 +387,13 @@ kv_gather_kernel(const GatherArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int head = blockIdx.y;
     const int64_t unit = blockIdx.x;
+    if (head == 0 && threadIdx.x >= kGatherThreads - 32) {  // 32 sequences a unit: there are more units than sequences
+        const int64_t i = unit * 32 + (threadIdx.x & 31);
+        if (i < a.seqs) check_sequence(a.cu, a.tokens, nullptr, i, a.err);
+    }
     const int seq = find_seq(a.cu, a.seqs, unit, kGatherTokens, 1);
     const int64_t t0 = a.cu[seq], t1 = a.cu[seq + 1];
-    if (t0 < 0 || t1 < t0 || t1 > a.tokens) {
-        if (threadIdx.x == 0) atomicOr(a.err, kErrBounds);
-        return;
-    }
+    if (t0 < 0 || t1 < t0 || t1 > a.tokens) return;  // latched by check_sequence
     const int64_t first = (unit - unit_base(a.cu, seq, kGatherTokens, 1)) * kGatherTokens;
     const int n = (int)min((int64_t)kGatherTokens, t1 - t0 - first);
     if (first < 0 || n <= 0) return;  // a unit before the first sequence, or that no sequence uses

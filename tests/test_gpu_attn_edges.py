@@ -1,0 +1,86 @@
+"""The cache and attention calls at their edges: bounds that no work unit meets, numbers that are not finite, what a
+pack's neighbours may change, waits that run out, a long sequence among many short ones.  Bounds of errors are those
+that tests/test_gpu_attn.py derives; what a test adds to them stands in its docstring."""
+import numpy as np
+import pytest
+
+import attn_reference as ref
+from helpers import cuda, lib, to_np, torch
+from test_gpu_attn import (append_case, bound, check_cache, check_decode, cu_of, decode_case, dev_cache, dtype, half_step,
+                           lse_bound, rounded, run_decode, same_bits, split)
+
+pytestmark = pytest.mark.gpu
+BLOCK = ref.BLOCK
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_cuda():
+    if not torch().cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    yield
+    assert lib().bitnet_get_device_error() == lib().BITNET_OK
+
+
+def ints(*x):
+    return cuda(np.array(x, np.int32))
+
+
+BAD_BOUNDS = [
+    # tokens, bounds: no work unit looks at the pair that is wrong
+    (2, [0, 1, 2, 3]),       # a unit for each token: the third sequence has none
+    (2, [0, 1, 0, 1]),       # ... and the second goes backwards between two that are found
+    (3, [-1, 0, 1, 2]),      # ... the first begins before row 0 and ends at it
+    (4, [0, 1, 2, 2, 5]),
+    (80, [0, 70, 10, 80]),   # units of 16 tokens: the second and third sequence begin at the same unit
+    (300, [0, 140, 20, 300]),
+]
+
+
+@pytest.mark.parametrize("tokens,bounds", BAD_BOUNDS)
+def test_bad_bounds_are_latched_by_every_packed_call(tokens, bounds):
+    b, tt = lib(), torch()
+    dim, hk, page, seqs = 64, 2, 16, len(bounds) - 1
+    host = ref.Cache(seqs * 20, hk, page, dim)
+    dev, table = dev_cache(host), cuda(np.arange(seqs * 20, dtype=np.int32).reshape(seqs, 20))
+    x, cu, good = tt.ones((tokens, hk, dim), device="cuda"), ints(*bounds), ints(*[0] * seqs, tokens)
+    zero = ints(*[0] * seqs)
+    x16, out = x.half(), tt.empty((tokens, hk, dim), device="cuda")
+    calls = {
+        "append": lambda c: b.bitnet_kv_append(dev, x, x, x, c, zero, table, out),
+        "gather": lambda c: b.bitnet_kv_gather(dev, c, table, out, tt.empty_like(out)),
+        "prompt, queries": lambda c: b.bitnet_attn_prompt(x16, x16, x16, c, good, out),
+        "prompt, keys": lambda c: b.bitnet_attn_prompt(x16, x16, x16, good, c, out),
+    }
+    for name, call in calls.items():
+        call(cu)
+        assert b.bitnet_get_device_error() == b.BITNET_ERR_VALUE, name
+        call(good)
+        assert b.bitnet_get_device_error() == b.BITNET_OK, name
+
+
+@pytest.mark.parametrize("wrong", [0, 1, 700, 2998, 2999])
+def test_one_bad_bound_among_many_sequences(wrong):
+    """3000 sequences of one token, one of them backwards; then a negative length of a sequence without new tokens."""
+    b, tt = lib(), torch()
+    dim, seqs = 64, 3000
+    dev = dev_cache(ref.Cache(seqs, 1, 16, dim))
+    x, out = tt.ones((seqs, 1, dim), device="cuda"), tt.empty((seqs, 1, dim), device="cuda")
+    table, old = tt.arange(seqs, dtype=tt.int32, device="cuda").view(-1, 1), tt.zeros(seqs, dtype=tt.int32, device="cuda")
+    cu = np.arange(seqs + 1, dtype=np.int32)
+    bad = cu.copy()
+    bad[wrong + 1] = bad[wrong] - 1 if wrong else -1
+    for c, o, want in ((bad, old, b.BITNET_ERR_VALUE), (cu, old, b.BITNET_OK)):
+        b.bitnet_kv_append(dev, x, x, x, cuda(c), o, table, out)
+        assert b.bitnet_get_device_error() == want
+    empty = cu.copy()
+    empty[wrong + 1:] -= 1   # no new token of that sequence
+    negative = old.clone()
+    negative[wrong] = -1
+    for o, want in ((negative, b.BITNET_ERR_VALUE), (old, b.BITNET_OK)):
+        b.bitnet_kv_append(dev, x[1:], x[1:], x[1:], cuda(empty), o, table, out[1:])
+        assert b.bitnet_get_device_error() == want
