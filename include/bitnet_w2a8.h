@@ -541,7 +541,7 @@ typedef struct {
  * -inf).  Scores, softmax and sums are fp32; the softmax weights are rounded
  * once to dtype, as operands of the second product (neighbouring rows of a
  * sequence share when a running maximum moves, so they may change a row's last
- * bits, never more).  out and lse may not overlap inputs.  Rows behind the last sequence are not written.  head_dim 64 or 128; rows 16-byte aligned, strides
+ * bits, never more; other sequences change nothing).  out and lse may not overlap inputs.  Rows behind the last sequence are not written.  head_dim 64 or 128; rows 16-byte aligned, strides
  * multiples of 8.
  * Errors: NULL, SHAPE, ALIGN, VALUE, UNSUPPORTED (not an sm_100 device), CUDA;
  * bounded device waits that run out latch BITNET_ERR_TIMEOUT. */

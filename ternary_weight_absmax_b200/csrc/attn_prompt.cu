@@ -407,6 +407,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const uint32_t ts = tmem + C::s_at(s) + quarter, to = tmem + C::o_at(s) + quarter;
         const float c = a.scale_log2;
         float ref = -INFINITY, l = 0.0f;
+        // Rows behind the sequence's last are another sequence's queries: no vote on the reference.
+        const float lag = r < lq ? kLag : INFINITY;
         int limit_col = lk;  // keys that the row sees
         if (a.causal) limit_col = min(lk, r + shift + 1);
         const int first_masked = (a.causal ? min(lk, r0 + shift + 1) : lk) / kKeys;  // tiles before it need no mask
@@ -441,6 +443,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         mx[q] = i + 4 < kKeys ? max3(mx[q], val(i + q), val(i + 4 + q)) : fmaxf(mx[q], val(i + q));
                 return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
             };
+            auto passed = [&](float m) { return __any_sync(0xffffffffu, (m - ref) * c > lag); };
             auto move_ref = [&](float m) {  // to m, where m is above it; sums and output follow
                 const float up = fmaxf(ref, m);
                 const float f = up == -INFINITY ? 1.0f : ex2((ref - up) * c);
@@ -466,7 +469,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const float m = row_max();
                 if (j == 0)
                     ref = m;
-                else if (__any_sync(0xffffffffu, (m - ref) * c > kLag))
+                else if (passed(m))
                     move_ref(m);
             }
             // At D = 128 the exponentials start with the reference as it is, and
@@ -512,7 +515,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                 mx[k] = i + 4 < kKeys ? max3(mx[k], val(i + k), val(i + 4 + k)) : fmaxf(mx[k], val(i + k));
                     }
                     const float m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-                    if (!__any_sync(0xffffffffu, (m - ref) * c > kLag)) break;
+                    if (!passed(m)) break;
                     move_ref(m);
                     set_ref();
                 }

@@ -84,3 +84,30 @@ def test_one_bad_bound_among_many_sequences(wrong):
     for o, want in ((negative, b.BITNET_ERR_VALUE), (old, b.BITNET_OK)):
         b.bitnet_kv_append(dev, x[1:], x[1:], x[1:], cuda(empty), o, table, out[1:])
         assert b.bitnet_get_device_error() == want
+
+
+def prompt(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None):
+    """(out, lse) of a call on device tensors; out fp32 unless a dtype is given."""
+    b, tt = lib(), torch()
+    o = tt.full(q.shape, 9.0, dtype=out or tt.float32, device="cuda")
+    lse = tt.full(q.shape[:2], 9.0, device="cuda")
+    b.bitnet_attn_prompt(q, k, v, ints(*cu_q), ints(*cu_k), o, causal=causal, scale=scale, lse=lse)
+    return o, lse
+
+
+@pytest.mark.parametrize("dim,t,causal", [(64, "f16", True), (64, "bf16", False), (128, "bf16", True), (128, "f16", False)])
+def test_prompt_bits_do_not_depend_on_the_queries_packed_behind(dim, t, causal):
+    """Rows behind a sequence's end in its last tile are the next sequence's queries: whatever those are (and NaN or
+    infinite), the sequence's own rows keep their bits."""
+    tt = torch()
+    rng = np.random.default_rng(15)
+    lens = [150, 106, 300]
+    cu = cu_of(lens)
+    q, k, v = (cuda(rng.normal(0, 1, (sum(lens), 4, dim)).astype(np.float32)).to(dtype(t)) for _ in range(3))
+    want = prompt(q, k, v, cu, cu, causal)
+    for i in range(3):
+        own = slice(int(cu[i]), int(cu[i + 1]))
+        for other in (200 * tt.randn_like(q), tt.full_like(q, float("nan")), tt.full_like(q, float("inf"))):
+            other[own] = q[own]
+            for a, w in zip(prompt(other, k, v, cu, cu, causal), want):
+                assert tt.equal(a[own], w[own]), f"sequence {i}"
