@@ -111,9 +111,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Maxima that are NaN where an operand is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ float max2(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
 // Two fp32 values in one 64-bit register, one instruction for both.
@@ -440,8 +446,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 for (int i = 4; i < kKeys; i += 8)
 #pragma unroll
                     for (int q = 0; q < 4; q++)
-                        mx[q] = i + 4 < kKeys ? max3(mx[q], val(i + q), val(i + 4 + q)) : fmaxf(mx[q], val(i + q));
-                return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+                        mx[q] = i + 4 < kKeys ? max3(mx[q], val(i + q), val(i + 4 + q)) : max2(mx[q], val(i + q));
+                return max2(max3(mx[0], mx[1], mx[2]), mx[3]);
             };
             auto passed = [&](float m) { return __any_sync(0xffffffffu, (m - ref) * c > lag); };
             auto move_ref = [&](float m) {  // to m, where m is above it; sums and output follow
@@ -512,9 +518,10 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         for (int i = 4 + 64 * q; i < min(kKeys, 68 + 64 * q); i += 8)
 #pragma unroll
                             for (int k = 0; k < 4; k++)
-                                mx[k] = i + 4 < kKeys ? max3(mx[k], val(i + k), val(i + 4 + k)) : fmaxf(mx[k], val(i + k));
+                                mx[k] = i + 4 < kKeys ? max3(mx[k], val(i + k), val(i + 4 + k)) : max2(mx[k], val(i + k));
                     }
-                    const float m = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+                    const float m = max2(max3(mx[0], mx[1], mx[2]), mx[3]);
+                    if (!(m < INFINITY)) l = NAN;  // a polynomial's weight of a NaN is 0
                     if (!passed(m)) break;
                     move_ref(m);
                     set_ref();
@@ -542,9 +549,11 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             ok = __all_sync(0xffffffffu, ok);
             ptx::tc_fence_after();
         }
-        if (ref == -INFINITY) l = 0.0f;  // a row without keys
+        // A row with a score that is NaN has l = NaN by now; one whose reference overflows
+        // has no softmax either.  A row without keys has l = 0.
+        if (!(ref * c < INFINITY)) l = NAN;
         if (ok) {
-            const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+            const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
             Out *dst = static_cast<Out *>(a.out) + ((q0 + r) * a.q_heads + h) * D;
 #pragma unroll
             for (int q = 0; q < D / 32; q++) {
@@ -555,12 +564,12 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     ptx::tmem_wait_ld();
                 }
 #pragma unroll
-                for (int i = 0; i < 32; i++) f[i] = l > 0.0f ? __uint_as_float(o[i]) * inv : 0.0f;
+                for (int i = 0; i < 32; i++) f[i] = l == 0.0f ? 0.0f : __uint_as_float(o[i]) * inv;
                 if (r < lq) store_from_f32<32>(dst + 32 * q, f);
             }
             if (a.lse && r < lq)
                 a.lse[(q0 + r) * a.q_heads + h] =
-                    l > 0.0f ? (ref * c + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                    l == 0.0f ? -INFINITY : (ref * c + log2f(l)) * 0.69314718055994531f;
         }
     }
     ptx::tc_fence_before();

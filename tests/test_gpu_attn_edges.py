@@ -111,3 +111,71 @@ def test_prompt_bits_do_not_depend_on_the_queries_packed_behind(dim, t, causal):
             other[own] = q[own]
             for a, w in zip(prompt(other, k, v, cu, cu, causal), want):
                 assert tt.equal(a[own], w[own]), f"sequence {i}"
+
+
+def check_rows(got, lse, q, k, v, seen, t, good):
+    """Rows x heads of `good` are within the bounds, of the sequences' own formula on q, k, v (numpy, finite); the others
+    are NaN in every element, and so are their lse."""
+    dim = q.shape[2]
+    o, z, mag, size, _ = ref.attend(q, k, v, dim ** -0.5, seen)
+    g, l = to_np(got.double()), to_np(lse.double())
+    assert np.isnan(g[~good]).all() and np.isnan(l[~good]).all()
+    err = np.abs(g - o)
+    assert np.all((err <= bound(mag, size, o, k.shape[0], dim, half_step(t), "f32"))[good])
+    some = good & np.isfinite(z)
+    assert np.all((np.abs(l - np.where(some, z, 0)) <= lse_bound(z, size, k.shape[0], dim))[some])
+    assert np.all(g[good & ~some] == 0) and np.all(np.isneginf(l[good & ~some]))
+
+
+NAN_PROMPTS = [(64, "f16", 300, True), (64, "bf16", 300, False), (128, "bf16", 300, True), (128, "f16", 300, False),
+               (128, "bf16", 3, True)]
+
+
+@pytest.mark.parametrize("dim,t,n,causal", NAN_PROMPTS)
+def test_prompt_nan_in_a_query_makes_its_row_nan(dim, t, n, causal):
+    rng = np.random.default_rng(16)
+    q, k, v = (rounded(rng.normal(0, 1, (n, 2, dim)).astype(np.float32), t) for _ in range(3))
+    bad = q.copy()
+    good = np.ones((n, 2), bool)
+    for r, h, e, x in ((0, 0, 5, np.nan), (1, 1, 0, np.nan), (n // 2, 0, dim - 1, np.nan), (n - 1, 1, 7, -np.nan)):
+        bad[r, h, e] = x
+        good[r, h] = False
+    seen = np.tril(np.ones((n, n), bool)) if causal else None
+    got, lse = prompt(*(cuda(x).to(dtype(t)) for x in (bad, k, v)), [0, n], [0, n], causal)
+    check_rows(got, lse, q, k, v, seen, t, good)
+
+
+@pytest.mark.parametrize("at", [0, 1, 5, 17, 40, 127, 130, 299])
+@pytest.mark.parametrize("dim,t,causal", [(64, "f16", True), (128, "bf16", True), (128, "f16", False)])
+def test_prompt_nan_in_a_key_makes_the_rows_that_see_it_nan(dim, t, causal, at):
+    """In every kind of column: the exponential is computed in two ways."""
+    n = 300
+    rng = np.random.default_rng(17)
+    q, k, v = (rounded(rng.normal(0, 1, (n, 2, dim)).astype(np.float32), t) for _ in range(3))
+    bad = k.copy()
+    bad[at, 1, 3] = np.nan
+    good = np.ones((n, 2), bool)
+    good[at if causal else 0:, 1] = False
+    seen = np.tril(np.ones((n, n), bool)) if causal else None
+    got, lse = prompt(*(cuda(x).to(dtype(t)) for x in (q, bad, v)), [0, n], [0, n], causal)
+    check_rows(got, lse, q, k, v, seen, t, good)
+
+
+@pytest.mark.parametrize("at", [2, 40, 200])
+@pytest.mark.parametrize("dim,t", [(64, "bf16"), (128, "bf16"), (128, "f16")])
+def test_prompt_infinite_scores(dim, t, at):
+    """One infinite element of a key: a score of +infinity has no softmax (NaN), one of -infinity is a key without weight."""
+    n = 300
+    rng = np.random.default_rng(18)
+    q, k, v = (rounded(rng.normal(0, 1, (n, 2, dim)).astype(np.float32), t) for _ in range(3))
+    bad = k.copy()
+    bad[at, 0, 9] = np.inf
+    seen = np.tril(np.ones((n, n), bool))
+    good = ~(seen[:, at][:, None] & (q[:, :, 9] > 0) & (np.arange(2) == 0))
+    assert np.all(q[:, 0, 9] != 0) and (~good).any() and good[at:, 0].any()
+    got, lse = prompt(*(cuda(x).to(dtype(t)) for x in (q, bad, v)), [0, n], [0, n])
+    for h, s in ((0, seen & (np.arange(n) != at)), (1, seen)):
+        low = good[:, h].copy()
+        if h == 0:
+            low[:at] = True
+        check_rows(got[:, h:h + 1], lse[:, h:h + 1], q[:, h:h + 1], k[:, h:h + 1], v[:, h:h + 1], s, t, low[:, None])
