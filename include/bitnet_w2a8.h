@@ -540,7 +540,9 @@ typedef struct {
  * later chunk behind a gathered prefix).  A row that sees no key gives 0 (lse
  * -inf); one with a score that is NaN or +inf (in units of log 2, so from 3.4e38
  * / 1.443 on) is NaN, its lse as well; a score of -inf is a key without weight.
- * Scores, softmax and sums are fp32; the softmax weights are rounded
+ * Keys and values that a row does not see may be anything, NaN and infinities
+ * included; where a row sees a value that is NaN or infinite, that element of its
+ * output is not finite.  Scores, softmax and sums are fp32; the softmax weights are rounded
  * once to dtype, as operands of the second product (neighbouring rows of a
  * sequence share when a running maximum moves, so they may change a row's last
  * bits, never more; other sequences change nothing).  out and lse may not overlap inputs.  Rows behind the last sequence are not written.  head_dim 64 or 128; rows 16-byte aligned, strides

@@ -17,7 +17,8 @@
 //                   slots half a step apart: with an issuer for each slot both
 //                   softmaxes ran at the same time, then both slots' MMAs
 //                   (566 us on 8192 tokens and 32 heads of 128).
-//   warps 10, 11    check the bounds of 32 sequences, then idle.
+//   warps 10, 11    check the bounds of 32 sequences, then V in the guarded tiles, beside
+//                   the softmax of the same tile.
 // Tensor memory: S0 | S1 | O0 | O1.
 //
 // The running maximum is only a reference: a row keeps it while its scores
@@ -27,8 +28,11 @@
 // PV of tile j-1 is (both are tracked by the commit after S), so O is free then.
 //
 // Scores outside a row's keys become -inf before they are used, so K rows of
-// other sequences never reach a row; V rows behind the sequence's last are set
-// to 0 in shared memory (0 times a stray NaN or infinity would not be 0).
+// other sequences never reach a row.  A weight of 0 times a NaN or infinity would
+// not be 0, so in the tiles that some row sees in part ("guarded": around the diagonal,
+// or past the sequence's end; the last few) warps 10 and 11 look over V before the MMA
+// takes it: rows behind the sequence's last become 0, and so does an element that is
+// not finite, whose column and first key are kept and added to the rows that see it.
 //
 // Bound: the tensor cores' 4 D operations a score at D = 128, the softmax (a
 // special function unit's exponential and about four instructions a score) at
@@ -40,6 +44,7 @@
 // Every wait is bounded; a CTA whose wait ran out latches the error word, ends
 // its copies and MMAs (bounded) and frees its tensor memory.
 #include <cudaTypedefs.h>
+#include <limits.h>
 #include <string.h>
 
 #include <atomic>
@@ -53,8 +58,9 @@ namespace {
 
 constexpr int kTile = 128;  // queries of a slot
 constexpr int kSlots = 2;
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kIdleWarp = 10;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kGuardWarp = 10;
 constexpr int kThreads = 384;  // three warpgroups: two softmax, one for loads and MMAs
+constexpr int kGuarded = 5;    // most guarded tiles of a CTA: 256 rows and 64 keys that do not begin with a tile
 constexpr int kParts = 2;      // the weights of a tile are handed to the MMA in two parts
 constexpr uint32_t kDrainLimit = 1u << 22;
 constexpr long long kDrainCycles = 2000000;  // ~1 ms
@@ -95,7 +101,8 @@ struct Cfg {
     static constexpr int kTileBytes = kHalves * kPiece;
     static constexpr int kOffKv = kSlots * kQBytes;
     static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
-    static constexpr size_t kSmem = 1024 + kOffBar + 256;
+    static constexpr int kOffFirst = kOffBar + 320;        // int[3][D]: first key of a column that is NaN, +inf, -inf
+    static constexpr size_t kSmem = 1024 + kOffFirst + 3 * D * 4;
     // Tensor-memory columns: S0 | S1 | O0 | O1.
     static constexpr int kTmemCols = kSlots * (kKeys + D);
     // Registers: softmax threads hold a row of scores, the others little; the
@@ -197,10 +204,14 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     auto p_full = [&](int s, int part) { return bars + 8u * (6 + kParts * s + part); };
     auto kv_full = [&](int t) { return bars + 8u * (6 + kSlots * kParts + t); };
     auto kv_empty = [&](int t) { return kv_full(kStages + t); };
-    const uint32_t v_fixed = kv_full(2 * kStages);
-    const uint32_t drain = v_fixed + 8u;
+    // V of a guarded tile lands here (each is used once) and is full, in kv_full, when both guards have arrived there.
+    auto v_land = [&](int g) { return kv_full(2 * kStages + g); };
+    const uint32_t drain = kv_full(2 * kStages + kGuarded);
+    static_assert((6 + kSlots * kParts + 2 * kStages + kGuarded + 1) * 8 + 12 <= C::kOffFirst - C::kOffBar, "barriers");
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + (drain + 8u - base));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *not_finite = abort_flag + 1;
+    int *first_at = reinterpret_cast<int *>(gbase + C::kOffFirst);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // What needs no memory of an earlier kernel comes before the wait for it.
@@ -212,12 +223,12 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             ptx::mbar_init(o_full(s), 1);
         }
         for (int t = 0; t < kStages; t++) {
-            ptx::mbar_init(kv_full(t), 1);
+            ptx::mbar_init(kv_full(t), 1 + (t & 1));  // odd stages hold V: two guards, or two arrivals of the loader
             ptx::mbar_init(kv_empty(t), 1);
         }
-        ptx::mbar_init(v_fixed, 1);
+        for (int g = 0; g < kGuarded; g++) ptx::mbar_init(v_land(g), 1);
         ptx::mbar_init(drain, 1);
-        *abort_flag = 0;
+        *abort_flag = *not_finite = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&map_q);
         ptx::prefetch_tmap(&map_k);
@@ -226,9 +237,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (warp >= kIdleWarp) {  // 32 sequences a CTA: there are more CTAs than sequences
+    if (warp >= kGuardWarp) {  // 32 sequences a CTA: there are more CTAs than sequences
         const int64_t i = (int64_t)blockIdx.x * 32 + lane;
-        const bool of_q = warp == kIdleWarp;
+        const bool of_q = warp == kGuardWarp;
         if (i < a.seqs) check_sequence(of_q ? a.cu_q : a.cu_k, of_q ? a.q_tokens : a.k_tokens, nullptr, i, a.err);
     }
 
@@ -260,6 +271,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         if (item >= items) row0[s] = lq;  // no such row: nothing is written
     }
     const int most = max(tiles[0], tiles[1]);
+    // Tiles before it are seen whole by every row of the slots.
+    const int guard0 = max(0, a.causal ? min(lk, row0[0] + shift + 1) : lk) / kKeys;
+    for (int i = threadIdx.x; i < 3 * D; i += kThreads) first_at[i] = INT_MAX;
     const uint32_t limit = *a.wait_limit;
 
     if (warp == kMmaWarp) {
@@ -280,10 +294,10 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == kTmaWarp) {
         // ------------------------------------------------ loads; step t: K of tile t / 2, then V
-        const int ragged = lk % kKeys;
-        const bool fix = ragged != 0 && most == (lk + kKeys - 1) / kKeys;  // the last V tile passes the sequence's end
-        int issued = 0;
         if (lane == 0) {
+            int issued = 0;
+            static_assert(kStages % 2 == 0, "a stage holds K only or V only");
+            auto guarded = [&](int t) { return (t & 1) && (t >> 1) >= guard0; };
             auto load = [&](uint32_t dst, const CUtensorMap *m, uint32_t bar, int h, int64_t row, int piece) {
                 ptx::mbar_arrive_expect_tx(bar, C::kHalves * piece);
 #pragma unroll
@@ -297,8 +311,10 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     ok = false;
                     break;
                 }
-                load(kv_at(t), (t & 1) ? &map_v : &map_k, kv_full(t % kStages), kvh, k0 + (int64_t)(t >> 1) * kKeys,
-                     C::kPiece);
+                const uint32_t full = kv_full(t % kStages);
+                load(kv_at(t), (t & 1) ? &map_v : &map_k, guarded(t) ? v_land((t >> 1) - guard0) : full, kvh,
+                     k0 + (int64_t)(t >> 1) * kKeys, C::kPiece);
+                if ((t & 1) && !guarded(t)) ptx::mbar_arrive(full);
                 issued++;
                 if (t == 0 && tiles[1]) load(base + C::kQBytes, &map_q, q_full(1), head[1], q0 + row0[1], C::kQPiece);
             }
@@ -309,19 +325,10 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 while (!ptx::mbar_try_wait(bar, parity))
                     if (clock64() - t0 > kDrainCycles) break;
             };
-            for (int t = max(0, issued - kStages); t < issued; t++) landed(kv_full(t % kStages), (t / kStages) & 1);
+            for (int t = max(0, issued - kStages); t < issued; t++)
+                guarded(t) ? landed(v_land((t >> 1) - guard0), 0) : landed(kv_full(t % kStages), (t / kStages) & 1);
             for (int s = 0; s < kSlots; s++)
                 if (tiles[s] && issued > 0) landed(q_full(s), 0);
-        }
-        issued = __shfl_sync(0xffffffffu, issued, 0);
-        if (fix && issued == 2 * most) {  // the whole warp: rows behind the last key of the last V tile
-            unsigned char *v = gbase + (kv_at(2 * most - 1) - base);
-            for (int p = 0; p < C::kHalves; p++)
-                for (int i = lane; i < (kKeys - ragged) * 8; i += 32)
-                    *reinterpret_cast<uint4 *>(v + p * C::kPiece + ragged * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(v_fixed);
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -332,7 +339,6 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         if (ptx::elect_one() && most > 0) {
             const uint32_t id_s = ptx::idesc_f16(kTile, kKeys, kBf16, false, a.neg != 0);
             constexpr uint32_t id_o = ptx::idesc_f16(kTile, D, kBf16, true);
-            const bool fix = lk % kKeys != 0 && most == (lk + kKeys - 1) / kKeys;
             const uint64_t dq = ptx::desc_k_sw128(base), dk = ptx::desc_k_sw128(base + C::kOffKv),
                            dv = ptx::desc_mn_sw128(base + C::kOffKv, C::kPiece);
             const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
@@ -373,7 +379,6 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         const bool got_k = more && ptx::mbar_try_wait(kv_full(tk), pk);
                         const bool got_b = ptx::mbar_try_wait(p_full(s, 1), j & 1);
                         wait(got_v, kv_full(tv), pv);
-                        if (fix && j == most - 1) wait(false, v_fixed, 0);
                         wait(got_a, p_full(s, 0), j & 1);
                         if (!ok) break;
                         ptx::tc_fence_after();
@@ -541,7 +546,13 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             unpack2(add2(sum[0], sum[1]), l0, l1);
             l += l0 + l1;
         }
+        bool hurt = false;  // values that are not finite, which the guards have taken out
         if (ok && n > 0) {
+            // The guards are done with the slot's last V (the slots' walks differ by 128
+            // rows, less than the ring holds: its stage has not gone on).
+            static_assert(kTile / kKeys < kStages / 2, "phase of the last V");
+            const int tv = 2 * n - 1;
+            hurt = ptx::mbar_wait(kv_full(tv % kStages), tv / kStages & 1, limit, abort_flag) && *not_finite;
             if (!ptx::mbar_wait(o_full(s), 0, limit, abort_flag)) {
                 give_up();
                 ok = false;
@@ -567,10 +578,79 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 for (int i = 0; i < 32; i++) f[i] = l == 0.0f ? 0.0f : __uint_as_float(o[i]) * inv;
                 if (r < lq) store_from_f32<32>(dst + 32 * q, f);
             }
+            if (hurt && r < lq) {
+#pragma unroll 1
+                for (int d = 0; d < D; d++) {
+                    float x = (float)dst[d];
+                    if (first_at[d] < limit_col) x = NAN;
+                    if (first_at[D + d] < limit_col) x += INFINITY;
+                    if (first_at[2 * D + d] < limit_col) x -= INFINITY;
+                    dst[d] = (Out)x;
+                }
+            }
             if (a.lse && r < lq)
                 a.lse[(q0 + r) * a.q_heads + h] =
                     l == 0.0f ? -INFINITY : (ref * c + log2f(l)) * 0.69314718055994531f;
         }
+    } else if (warp >= kGuardWarp) {
+        // ------------------------------------------------ V of the guarded tiles
+        // Bound: the softmax beside it, whose time it mostly fits in.  3 prompts of up to 150
+        // tokens take 9.7 us with it and 9.3 without, 8192 tokens the same; 16 ragged ones of
+        // heads of 64 take 73 and 69, as long when no tile is guarded: the code around
+        // is compiled otherwise.  (More loads at once in a lane: 9.6 us, but 451 us against 444 on 8192.)
+        using P2 = typename Pair<T>::type;
+        constexpr int kPieceChunks = C::kPiece / 16;
+        constexpr uint32_t kInf = kBf16 ? 0x7f80u : 0x7c00u;
+        const int me = (warp - kGuardWarp) * 32 + lane;
+        for (int g = 0; g < most - guard0; g++) {
+            bool ok = ptx::mbar_wait(v_land(g), 0, limit, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                if (lane == 0) give_up();
+                break;
+            }
+            const int key0 = (guard0 + g) * kKeys, keys = lk - key0;  // from this tile on
+            uint4 *v = reinterpret_cast<uint4 *>(gbase + (kv_at(2 * (guard0 + g) + 1) - base));
+            // 16-byte chunk e of a piece is number e & 7 (swizzled) of row e / 8.
+            const int own = min(keys, kKeys) * 8;
+            P2 sum[4];  // of 0 times the values: NaN if one is not finite
+#pragma unroll
+            for (int i = 0; i < 4; i++) sum[i] = Pair<T>::down(0.0f, 0.0f);
+#pragma unroll 1
+            for (int p = 0; p < C::kHalves; p++) {
+                uint4 *piece = v + p * kPieceChunks;
+#pragma unroll 1
+                for (int e = own + me; e < kPieceChunks; e += 64) piece[e] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                for (int e = me; e < own; e += 64) {
+                    const uint4 x = piece[e];
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        sum[k] = __hfma2(*reinterpret_cast<const P2 *>(&w[k]), Pair<T>::down(0.0f, 0.0f), sum[k]);
+                }
+            }
+            const float2 all = up2(__hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3])));
+            if (__any_sync(0xffffffffu, !(all.x + all.y == 0.0f))) {
+#pragma unroll 1
+                for (int e = me; e < C::kHalves * kPieceChunks; e += 64) {
+                    const int row = e / 8 & (kKeys - 1), column = e / kPieceChunks * 64 + ((e ^ row) & 7) * 8;
+                    unsigned short *x = reinterpret_cast<unsigned short *>(v + e);
+#pragma unroll 1
+                    for (int i = 0; i < 8; i++) {
+                        if ((x[i] & kInf) != kInf) continue;
+                        const int kind = (x[i] & 0x7fffu) != kInf ? 0 : x[i] == kInf ? 1 : 2;
+                        atomicMin(first_at + kind * D + column + i, key0 + row);
+                        x[i] = 0;
+                    }
+                }
+                if (lane == 0) *not_finite = 1;
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(kv_full((2 * (guard0 + g) + 1) % kStages));
+        }
+        __syncwarp();
     }
     ptx::tc_fence_before();
     __syncthreads();

@@ -179,3 +179,51 @@ def test_prompt_infinite_scores(dim, t, at):
         if h == 0:
             low[:at] = True
         check_rows(got[:, h:h + 1], lse[:, h:h + 1], q[:, h:h + 1], k[:, h:h + 1], v[:, h:h + 1], s, t, low[:, None])
+
+
+@pytest.mark.parametrize("dim,t,lq,lk,group", [
+    (64, "f16", 300, 300, 2), (64, "bf16", 250, 300, 3), (128, "bf16", 300, 300, 2), (128, "f16", 100, 333, 4),
+    (128, "bf16", 400, 400, 1), (64, "f16", 400, 130, 1), (128, "bf16", 5, 5, 4),
+])
+def test_values_that_a_row_does_not_see_may_be_anything(dim, t, lq, lk, group):
+    """NaN and infinities among the values: a row before them keeps its bits; one that sees them has NaN, or the
+    infinity, in their columns, and keeps the bits of the others."""
+    tt = torch()
+    rng = np.random.default_rng(19)
+    hk = 2
+    q = cuda(rng.normal(0, 1, (lq, hk * group, dim)).astype(np.float32)).to(dtype(t))
+    k, v = (cuda(rng.normal(0, 1, (lk, hk, dim)).astype(np.float32)).to(dtype(t)) for _ in range(2))
+    clean, lse = prompt(q, k, v, [0, lq], [0, lk])
+    inf, nan = float("inf"), float("nan")
+    marks = [(lk - 1, 0, 0, nan), (lk - 1, 1, dim - 1, inf), (max(0, lk - 2), 0, 1, -inf), (lk // 2, 0, 2, inf),
+             (lk // 2 + 1, 0, 2, -inf), (lk * 2 // 3, 1, 33, nan), (lk * 3 // 4, 1, 8, -inf)]
+    for many in (marks[:1], marks[1:2], marks):
+        dirty = v.clone()
+        first = np.full((hk, dim), lk + 1)
+        for at, h, e, x in many:
+            dirty[at, h, e] = x
+            first[h, e] = min(first[h, e], at)
+        got, l2 = prompt(q, k, dirty, [0, lq], [0, lk])
+        assert tt.equal(l2, lse)
+        last = np.arange(lq) + lk - lq  # the last key that a row sees
+        sees = cuda(np.repeat(first, group, 0)[None] <= last[:, None, None])
+        assert tt.equal(got[~sees], clean[~sees])
+        assert not bool(tt.isfinite(got[sees]).any())
+    # the whole of the last row, seen by the last query alone (or by none)
+    dirty = v.clone()
+    dirty[lk - 1] = nan
+    got, _ = prompt(q, k, dirty, [0, lq], [0, lk])
+    assert tt.equal(got[:lq - 1], clean[:lq - 1]) and bool(tt.isnan(got[lq - 1]).all())
+
+
+@pytest.mark.parametrize("dim,t", [(64, "f16"), (128, "bf16")])
+def test_an_infinite_value_is_the_rows_that_see_it(dim, t):
+    """Around the diagonal the sign is kept: +inf, -inf, and NaN where both are seen."""
+    n = 96
+    rng = np.random.default_rng(20)
+    q, k, v = (cuda(rng.normal(0, 1, (n, 1, dim)).astype(np.float32)).to(dtype(t)) for _ in range(3))
+    v[50, 0, 3], v[60, 0, 3], v[70, 0, 4] = float("inf"), float("-inf"), float("-inf")
+    got, _ = prompt(q, k, v, [0, n], [0, n])
+    g = to_np(got)[:, 0]
+    assert np.isfinite(g[:50]).all() and np.isposinf(g[50:60, 3]).all() and np.isnan(g[60:, 3]).all()
+    assert np.isfinite(g[:70, 4]).all() and np.isneginf(g[70:, 4]).all()
