@@ -542,7 +542,8 @@ typedef struct {
  * / 1.443 on) is NaN, its lse as well; a score of -inf is a key without weight.
  * Keys and values that a row does not see may be anything, NaN and infinities
  * included; where a row sees a value that is NaN or infinite, that element of its
- * output is not finite.  Scores, softmax and sums are fp32; the softmax weights are rounded
+ * output is not finite.  (F16: a weight below 2^-21 of the largest so far is held
+ * to 2^-32 of it.)  Scores, softmax and sums are fp32; the softmax weights are rounded
  * once to dtype, as operands of the second product (neighbouring rows of a
  * sequence share when a running maximum moves, so they may change a row's last
  * bits, never more; other sequences change nothing).  out and lse may not overlap inputs.  Rows behind the last sequence are not written.  head_dim 64 or 128; rows 16-byte aligned, strides

@@ -22,7 +22,7 @@
 // Tensor memory: S0 | S1 | O0 | O1.
 //
 // The running maximum is only a reference: a row keeps it while its scores
-// exceed it by less than 2^8, which leaves the weights well inside fp16 and
+// exceed it by less than 2^8, which leaves the weights inside fp16 (scaled, see kUp) and
 // bf16, so O is rescaled (by the slot's softmax warps, in place) a few times per
 // row at most instead of once per tile.  S of tile j complete means that
 // PV of tile j-1 is (both are tracked by the commit after S), so O is free then.
@@ -65,6 +65,11 @@ constexpr int kParts = 2;      // the weights of a tile are handed to the MMA in
 constexpr uint32_t kDrainLimit = 1u << 22;
 constexpr long long kDrainCycles = 2000000;  // ~1 ms
 constexpr float kLag = 8.0f;                 // log2 units that scores may exceed the reference maximum by
+// Weights are held at 2^kUp of their size.  fp16's would leave the normal numbers at 2^-14 of
+// the reference and end at 2^-25, and a prompt's many small ones beside a large one
+// are lost; from 2^(kLag + kUp) = 2^15 down to 2^-21 they are normal now.
+template <typename T>
+constexpr float kUp = std::is_same<T, __half>::value ? 7.0f : 0.0f;
 
 struct Args {
     const int32_t *cu_q, *cu_k;
@@ -505,7 +510,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             };
             auto set_ref = [&]() {
                 const float mc = ref == -INFINITY ? 0.0f : ref * c;
-                mc2 = pack2(-mc, -mc);
+                mc2 = pack2(kUp<T> - mc, kUp<T> - mc);
                 sum[0] = sum[1] = 0;
             };
             set_ref();
@@ -590,7 +595,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             }
             if (a.lse && r < lq)
                 a.lse[(q0 + r) * a.q_heads + h] =
-                    l == 0.0f ? -INFINITY : (ref * c + log2f(l)) * 0.69314718055994531f;
+                    l == 0.0f ? -INFINITY : (ref * c + (log2f(l) - kUp<T>)) * 0.69314718055994531f;
         }
     } else if (warp >= kGuardWarp) {
         // ------------------------------------------------ V of the guarded tiles

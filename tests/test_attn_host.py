@@ -269,3 +269,20 @@ def test_prompt_exponential_polynomial_ends_in_zero():
     assert (bits[y <= -127] == 0).all()
     small = bits[(y > -127) & (y < -126)].view(np.float32)
     assert (small >= 0).all() and (small <= 2.0 ** -126).all()
+
+
+def test_prompt_exponential_polynomial_up_to_the_largest_weight():
+    """Weights reach 2^(lag + up): the polynomial keeps its bound there, and fp16 holds them."""
+    import re
+    src = open(os.path.join(ROOT, "ternary_weight_absmax_b200", "csrc", "attn_prompt.cu")).read()
+    top = sum(float(re.search(p, src).group(1)) for p in (r"kLag = (\d+\.\d)f", r"__half>::value \? (\d+\.\d)f"))
+    body = src[src.index("uint64_t ex2_poly"):]
+    c = [np.float32(x) for x in re.findall(r"pack2\((0\.\d+)f, \1f\)", body[:body.index("\n}\n")])]
+    y = np.linspace(8.0, top + 2.0 ** -10, 100001).astype(np.float32)
+    n = np.rint(y)
+    r, p = (y - n).astype(np.float32), c[0]
+    for k in (*c[1:], np.float32(1.0)):
+        p = (p.astype(np.float64) * r + k).astype(np.float32)
+    got = np.ldexp(p.astype(np.float64), n.astype(int))
+    assert np.abs(got / np.exp2(y.astype(np.float64)) - 1.0).max() <= 2.0 ** -18.4 + 5 * 1.5 * 2.0 ** -24
+    assert got.max() < 65504

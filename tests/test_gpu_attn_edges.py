@@ -227,3 +227,30 @@ def test_an_infinite_value_is_the_rows_that_see_it(dim, t):
     g = to_np(got)[:, 0]
     assert np.isfinite(g[:50]).all() and np.isposinf(g[50:60, 3]).all() and np.isnan(g[60:, 3]).all()
     assert np.isfinite(g[:70, 4]).all() and np.isneginf(g[70:, 4]).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("gap", [12.0, 18.0, 22.0, 25.0])
+def test_prompt_fp16_weights_far_below_the_largest(dim, gap):
+    """One key with nearly all the weight and a value of 0, 4095 others 2^-gap below it that make up the output.
+
+    A weight is held in fp16 at 2^7 times its size relative to the row's reference (which the largest weight exceeds by
+    2^8 at most, so that it stays below 2^15): within fp16's half step, 2^-11 of it, from 2^-21 of the largest up, and
+    within half of fp16's smallest step below, 2^-25 / 2^7 = 2^-32 of the reference.  Here the first tile holds the
+    largest score, which is the reference, so the floor is at most 2^-32 sum |v| (the sum of weights being at least 1)."""
+    tt = torch()
+    n, rows = 4096, 40
+    rng = np.random.default_rng(21)
+    q, k = np.zeros((rows, 1, dim), np.float32), np.zeros((n, 1, dim), np.float32)
+    q[:, 0, 0], k[:, 0, 0] = 1.0, -gap / np.log2(np.e)
+    q[:, 0, 1], k[:, 0, 1] = rng.uniform(0.5, 1, rows), rng.uniform(-1, 0, n)
+    k[7] = 0.0
+    v = rng.uniform(0.5, 1.5, (n, 1, dim)).astype(np.float32)
+    v[7] = 0.0
+    q, k, v = (rounded(x, "f16") for x in (q, k, v))
+    got, _ = prompt(*(cuda(x).half() for x in (q, k, v)), [0, rows], [0, n], causal=False, scale=1.0)
+    o, _, mag, size, _ = ref.attend(q, k, v, 1.0)
+    floor = 2.0 ** -32 * np.abs(v.astype(np.float64)).sum(0)
+    err = np.abs(to_np(got.double()) - o)
+    tol = bound(mag, size, o, n, dim, half_step("f16"), "f32", floor)
+    assert np.all(err <= tol), f"{np.max(err / tol):.3g} of the bound"
