@@ -499,8 +499,8 @@ bitnet_status bitnet_kv_gather(const bitnet_kv_cache *cache, const int32_t *cu_t
  * weights as two fp16 parts (BF16: one), codes as themselves.  q rows of
  * q_stride elements, out contiguous [seqs][q_heads][dim], both of `dtype`; lse
  * (nullable) fp32 [seqs][q_heads] receives the natural logarithm of the sum of
- * exponentials.  No tokens: out is 0, lse -inf.  out and lse may not overlap
- * inputs.
+ * exponentials.  No tokens: out is 0, lse -inf; a head of q that holds a NaN or
+ * an infinity: both NaN.  out and lse may not overlap inputs.
  * workspace: bitnet_attn_decode_workspace_bytes(...) bytes, 16-byte aligned,
  * caller owned, contents undefined between calls.  Calls that share it must not
  * overlap on the GPU (two graphs that are replayed side by side need one each).

@@ -34,6 +34,12 @@ cudaError_t launch_attn_decode(const DecodeCall &d, const DeviceGlobals &g, cuda
 cudaError_t launch_attn_prompt(const bitnet_attn_prompt_args &a, const DeviceGlobals &g, cudaStream_t st);
 
 #ifdef __CUDACC__
+// The larger; NaN where an operand is (fmaxf gives the other operand).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
 // N consecutive elements as fp32 (one vector load), and back with one rounding each.
 template <int N>
 __device__ __forceinline__ void load_f32(const float *p, float (&v)[N]) {

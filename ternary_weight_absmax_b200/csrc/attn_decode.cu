@@ -175,11 +175,11 @@ __device__ __forceinline__ int exponent(float x) { return ((__float_as_int(x) >>
 // N output elements from their weighted sum, and the row's lse where it is asked for.
 template <int N, typename T>
 __device__ __forceinline__ void finish(T *out, float *lse, float m, float l, float (&s)[N]) {
-    const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+    const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);  // no tokens: 0; a score that is NaN: NaN
 #pragma unroll
     for (int k = 0; k < N; k++) s[k] *= inv;
     store_from_f32<N>(out, s);
-    if (lse) *lse = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (lse) *lse = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 template <int D, typename T>
@@ -376,13 +376,15 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         uint32_t qb[kBytes][2 * kK];
         float factor[2];  // of the scores of heads 2c, 2c + 1
         {
+            // A query that is not finite makes m NaN or infinite, its integers 0 and,
+            // by 0 times the factor, every score NaN.
             float m = 1e-30f;
 #pragma unroll
             for (int e = 0; e < 2 * kK; e++)
 #pragma unroll
-                for (int i = 0; i < 4; i++) m = fmaxf(m, fabsf(qv[e][i]));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                for (int i = 0; i < 4; i++) m = max_nan(m, fabsf(qv[e][i]));
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const float up = __fdiv_rn(kLargest, m), row = a.scale_log2 * __fdiv_rn(m, kLargest);
             factor[0] = __shfl_sync(0xffffffffu, row, 8 * c);
             factor[1] = __shfl_sync(0xffffffffu, row, 8 * c + 4);
@@ -660,9 +662,9 @@ attn_decode_join_kernel(const Args a, int64_t units) {
     T *out = static_cast<T *>(a.out) + row * D + d;
     float *lse = a.lse && d == 0 ? a.lse + row : nullptr;
     if constexpr (V == 1) {
-        const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+        const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
         *out = (T)(s[0] * inv);
-        if (lse) *lse = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (lse) *lse = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     } else {
         finish<V>(out, lse, m, l, s);
     }

@@ -123,15 +123,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Maxima that are NaN where an operand is.
+// NaN where an operand is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-    return y;
-}
-__device__ __forceinline__ float max2(float a, float b) {
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
 // Two fp32 values in one 64-bit register, one instruction for both.
@@ -456,8 +451,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 for (int i = 4; i < kKeys; i += 8)
 #pragma unroll
                     for (int q = 0; q < 4; q++)
-                        mx[q] = i + 4 < kKeys ? max3(mx[q], val(i + q), val(i + 4 + q)) : max2(mx[q], val(i + q));
-                return max2(max3(mx[0], mx[1], mx[2]), mx[3]);
+                        mx[q] = i + 4 < kKeys ? max3(mx[q], val(i + q), val(i + 4 + q)) : max_nan(mx[q], val(i + q));
+                return max_nan(max3(mx[0], mx[1], mx[2]), mx[3]);
             };
             auto passed = [&](float m) { return __any_sync(0xffffffffu, (m - ref) * c > lag); };
             auto move_ref = [&](float m) {  // to m, where m is above it; sums and output follow
@@ -528,9 +523,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         for (int i = 4 + 64 * q; i < min(kKeys, 68 + 64 * q); i += 8)
 #pragma unroll
                             for (int k = 0; k < 4; k++)
-                                mx[k] = i + 4 < kKeys ? max3(mx[k], val(i + k), val(i + 4 + k)) : max2(mx[k], val(i + k));
+                                mx[k] = i + 4 < kKeys ? max3(mx[k], val(i + k), val(i + 4 + k)) : max_nan(mx[k], val(i + k));
                     }
-                    const float m = max2(max3(mx[0], mx[1], mx[2]), mx[3]);
+                    const float m = max_nan(max3(mx[0], mx[1], mx[2]), mx[3]);
                     if (!(m < INFINITY)) l = NAN;  // a polynomial's weight of a NaN is 0
                     if (!passed(m)) break;
                     move_ref(m);

@@ -254,3 +254,21 @@ def test_prompt_fp16_weights_far_below_the_largest(dim, gap):
     err = np.abs(to_np(got.double()) - o)
     tol = bound(mag, size, o, n, dim, half_step("f16"), "f32", floor)
     assert np.all(err <= tol), f"{np.max(err / tol):.3g} of the bound"
+
+
+@pytest.mark.parametrize("dim,t,group", [(128, "f32", 4), (128, "bf16", 1), (64, "f16", 8), (64, "f32", 12)])
+@pytest.mark.parametrize("bad", [np.nan, -np.nan, np.inf, -np.inf])
+def test_decode_queries_that_are_not_finite(dim, t, group, bad):
+    """The head's output and lse are NaN (an infinite query has scores of both signs here); the others keep their bits."""
+    lens = [700, 1, 0, 5000, 33]
+    cache, table, q = decode_case(dim, t, 16, 2, group, lens, seed=41)
+    dev = dev_cache(cache)
+    want, wl = run_decode(dev, q, lens, table, t)
+    dirty = q.copy()
+    good = np.ones(q.shape[:2], bool)
+    for i, h, e in ((0, 0, 0), (3, group, dim - 1), (4, 2 * group - 1, 17), (2, 0, 3)):
+        dirty[i, h, e] = bad
+        good[i, h] = lens[i] == 0   # no keys: 0, whatever the query
+    got, lse = run_decode(dev, dirty, lens, table, t)
+    assert np.array_equal(got[good], want[good]) and np.array_equal(lse[good], wl[good])
+    assert np.isnan(got[~good]).all() and np.isnan(lse[~good]).all()
