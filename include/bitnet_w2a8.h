@@ -468,6 +468,9 @@ typedef struct {
  *             tokens', and if it falls the old codes become
  *             rint(code * (new / old))
  *   code      clamp(rint(x * scale), -127, 127), ties to even
+ * A block and head that is given a NaN or an infinity (in k after norm and
+ * rotation, or in v) has the scale NaN and any codes: all 16 tokens read as NaN
+ * until the block is written from its first token again.
  * q_out, k_out and v_out are rounded once to out_dtype (from the values before
  * quantisation).  Pages that a call writes belong to one sequence; pages that
  * sequences share (a common prefix) may only lie before the block of its first

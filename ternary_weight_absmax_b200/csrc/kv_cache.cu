@@ -136,7 +136,7 @@ struct Turn {
 
 // rint(x * s), |x * s| at most 127 and a rounding (s is 127 over an absmax of at
 // least |x|, or smaller, so the definition's clamp changes nothing): the low byte
-// of the sum with 1.5 2^23.
+// of the sum with 1.5 2^23.  (Where s is NaN any byte will do.)
 __device__ __forceinline__ uint32_t quant(float x, float s) {
     return __float_as_uint(__fadd_rn(__fmul_rn(x, s), 12582912.0f));
 }
@@ -146,13 +146,17 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, u
 
 // A new scale for a block that holds older tokens: the smaller one, and by how
 // much its old codes have to shrink.
+// NaN, once there, stays (1e-5 bounds a real scale, so the sum is finite).
 __device__ __forceinline__ float joint_scale(float s, float was, float &fall) {
-    s = fminf(s, was);
+    const float both = s + was;
+    s = both == both ? fminf(s, was) : both;
     fall = s < was ? __fdiv_rn(s, was) : 1.0f;
     return s;
 }
+// NaN for a block that holds a NaN or an infinity: codes have no such values, and
+// those that they would turn into are not told from real ones.
 __device__ __forceinline__ float block_scale(float amax) {
-    return __fmul_rn(127.0f, __frcp_rn(amax > kEps ? amax : kEps));
+    return amax < INFINITY ? __fmul_rn(127.0f, __frcp_rn(amax > kEps ? amax : kEps)) : NAN;
 }
 // codes <- rint(codes * fall): `rows` rows from p on, by `threads` threads.
 template <int D>
@@ -173,10 +177,10 @@ __device__ __forceinline__ void store_codes(int8_t *dst, const float (&x)[V], fl
 }
 template <int V>
 __device__ __forceinline__ float absmax(const float (&x)[V]) {
-    float m = 0.0f;
+    unsigned m = 0;  // not negative: ordered as integers, NaN above all others
 #pragma unroll
-    for (int k = 0; k < V; k++) m = fmaxf(m, fabsf(x[k]));
-    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // not negative: ordered as integers
+    for (int k = 0; k < V; k++) m = max(m, __float_as_uint(fabsf(x[k])));
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, m));
 }
 
 template <int D, typename In, typename Out, int kWarps>

@@ -272,3 +272,73 @@ def test_decode_queries_that_are_not_finite(dim, t, group, bad):
     got, lse = run_decode(dev, dirty, lens, table, t)
     assert np.array_equal(got[good], want[good]) and np.array_equal(lse[good], wl[good])
     assert np.isnan(got[~good]).all() and np.isnan(lse[~good]).all()
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("side", ["k", "v"])
+@pytest.mark.parametrize("new", [[1, 1, 1], [1, 40, 3], [9, 1, 100]])
+def test_append_of_numbers_that_are_not_finite(bad, side, new):
+    """The block's scale is NaN, so that all that is read of it is; other heads and blocks keep the definition's bits, a
+    later token of the block does not bring the scale back, and a page's next owner does."""
+    b, tt = lib(), torch()
+    dim, hk, group, page, old = 64, 3, 2, 32, [5, 0, 20]
+    cache, table, qkv, _, _ = append_case(dim, "f32", 0, False, page, hk, group, [n + 1 for n in new], old, seed=51)
+    n = sum(new)
+    dev = dev_cache(cache)
+    parts = [x[:n].copy() for x in split(qkv, hk * group, hk, dim)]
+    dirty = [x.copy() for x in parts]
+    which = 1 if side == "k" else 2
+    cu = cu_of(new)
+    at, head = int(cu[2]), 1      # the first new token of the last sequence: position 20, block 1, four older tokens
+    dirty[which][at, head, 11] = bad
+    outs = [tt.empty(x.shape, device="cuda") for x in parts]
+    b.bitnet_kv_append(dev, *(cuda(x) for x in dirty), cuda(cu), ints(*old), cuda(table), *outs)
+    ref.append(cache, *parts, cu, old, table)
+    for o, x in zip(outs, dirty):
+        same_bits(to_np(o), x, "outputs")
+
+    def check(what):
+        page0 = table[2][0]
+        for name in ("k", "v", "k_scale", "v_scale"):
+            got, want = to_np(getattr(dev, name)).copy(), getattr(cache, name).copy()
+            if name[0] == side:
+                if name[1:]:
+                    assert np.isnan(got[page0, head, 1]), what
+                    got[page0, head, 1] = want[page0, head, 1] = 0
+                else:
+                    got[page0, head, 16:32] = want[page0, head, 16:32] = 0
+            same_bits(got, want, f"{what}: {name}")
+
+    check("append")
+    total = [a + c for a, c in zip(old, new)]
+    rows = {s: tt.empty((sum(total), hk, dim), device="cuda") for s in "kv"}
+    b.bitnet_kv_gather(dev, cuda(cu_of(total)), cuda(table), rows["k"], rows["v"])
+    block = slice(sum(total[:2]) + 16, sum(total[:2]) + min(32, total[2]))
+    for s in "kv":
+        nan = tt.isnan(rows[s])
+        want = tt.zeros_like(nan)
+        if s == side:
+            want[block, head] = True
+        assert tt.equal(nan, want), s
+    q = rounded(np.random.default_rng(3).normal(0, 1, (3, hk * group, dim)).astype(np.float32), "f32")
+    got, lse = run_decode(dev, q, total, table, "f32")
+    hurt = np.zeros(got.shape[:2], bool)
+    hurt[2, head * group:(head + 1) * group] = True
+    assert np.isnan(got[hurt]).all() and np.isfinite(got[~hurt]).all()
+    assert np.isnan(lse[hurt]).all() if side == "k" else np.isfinite(lse).all()
+    # one finite token more for each sequence
+    more = [x[n:n + 3].copy() for x in split(qkv, hk * group, hk, dim)]
+    b.bitnet_kv_append(dev, *(cuda(x) for x in more), ints(0, 1, 2, 3), ints(*total), cuda(table),
+                       tt.empty((3, hk * group, dim), device="cuda"))
+    ref.append(cache, *more, [0, 1, 2, 3], total, table)
+    check("a token more")
+    # the page from its start, by another sequence
+    b.bitnet_kv_append(dev, *(cuda(x[:3]) for x in more), ints(0, 3), ints(16), cuda(table[2:]),
+                       tt.empty((3, hk * group, dim), device="cuda"))
+    ref.append(cache, *more, [0, 3], [16], table[2:])
+    page0 = table[2][0]
+    for name in ("k_scale", "v_scale"):
+        assert np.isfinite(to_np(getattr(dev, name))[page0, :, 1]).all()
+        same_bits(to_np(getattr(dev, name))[page0, :, 1], getattr(cache, name)[page0, :, 1], name)
+    for name in ("k", "v"):
+        same_bits(to_np(getattr(dev, name))[page0, :, 16:19], getattr(cache, name)[page0, :, 16:19], name)
