@@ -566,7 +566,8 @@ bitnet_status bitnet_get_device_error(bitnet_stream_t stream);
 
 /* Test hook: sets the iteration cap of the device-side bounded waits on the
  * current device (0 restores the default).  A tiny cap makes a wait run out
- * without hanging anything, so the timeout path can be exercised. */
+ * without hanging anything, so the timeout path can be exercised (at 1 every
+ * wait of bitnet_attn_decode runs out: it is not tried at all). */
 bitnet_status bitnet_set_wait_limit(uint32_t max_iterations);
 
 #ifdef __cplusplus

@@ -209,7 +209,9 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const uint32_t limit = *a.wait_limit;
+    // A try may be suspended for as long as a copy takes: at a cap of one a wait has
+    // none, and runs out for certain.
+    const uint32_t limit = *a.wait_limit - 1;
     uint32_t tile_no = 0;  // tiles that this warp has asked for: the stage and its phase
     bool ok = true;        // no wait has run out
 

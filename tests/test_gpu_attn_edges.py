@@ -342,3 +342,29 @@ def test_append_of_numbers_that_are_not_finite(bad, side, new):
         same_bits(to_np(getattr(dev, name))[page0, :, 1], getattr(cache, name)[page0, :, 1], name)
     for name in ("k", "v"):
         same_bits(to_np(getattr(dev, name))[page0, :, 16:19], getattr(cache, name)[page0, :, 16:19], name)
+
+
+@pytest.mark.parametrize("dim,t,lens", [(128, "f32", [5000, 900, 0]), (64, "bf16", [1]), (128, "f16", [40000])])
+def test_decode_wait_that_runs_out(dim, t, lens):
+    """A cap of one leaves no try: every warp with a tile gives up, waits for its copies and returns, and TIMEOUT is
+    latched; the next call on the same workspace has the bits of one before."""
+    b, tt = lib(), torch()
+    cache, table, q = decode_case(dim, t, 32, 2, 4, lens, seed=61)
+    dev = dev_cache(cache)
+    ws = tt.zeros(b.bitnet_attn_decode_workspace_bytes(len(lens), 8, 2, dim), dtype=tt.uint8, device="cuda")
+    want, wl = run_decode(dev, q, lens, table, t, ws)
+    check_decode(cache, table, q, lens, t, want, wl)
+    for _ in range(2):
+        b.bitnet_set_wait_limit(1)
+        try:
+            for _ in range(4):
+                run_decode(dev, q, lens, table, t, ws)
+            st = b.bitnet_get_device_error()
+        finally:
+            b.bitnet_set_wait_limit(0)
+        assert st == b.BITNET_ERR_TIMEOUT
+        assert b.bitnet_get_device_error() == b.BITNET_OK
+        got, lse = run_decode(dev, q, lens, table, t, ws)
+        assert b.bitnet_get_device_error() == b.BITNET_OK
+        assert np.array_equal(got, want) and np.array_equal(lse, wl)
+    check_cache(dev, cache, "after")
