@@ -583,32 +583,20 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     }
 }
 
-// Joins the units that lie in parts.  W warps take head blockIdx.y of a unit, a
-// lane holding D / (32 Z) elements of slice blockIdx.z, and join every W-th part,
-// several of them in flight; then the first of the warps joins the warps.
-template <int D, typename T, int W, int Z>
-__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
-attn_decode_join_kernel(const Args a, int64_t units) {
-    constexpr int V = D / (32 * Z), kFlight = V == 1 ? 12 : 8;
-    __shared__ float sm[W], sl[W], sums[W][32 * V];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t u = W == 1 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x;
-    if (u >= units) return;
-    const Split sp = a.splits[u];
-    const int of_seq = a.kv_heads * a.chunks, seq = (int)(u / of_seq), unit = (int)(u % of_seq);
-    const int kvh = unit / a.chunks, chunk = unit % a.chunks;
-    if (sp.parts < 2 || h >= a.group - chunk * a.per_chunk) return;
-    const int w = W == 1 ? 0 : warp, d = blockIdx.z * 32 * V + lane * V;
-    float m = -INFINITY, l = 0.0f, s[V];
+// Joins parts k, k + step, ... of a unit's head h, elements d .. d + V - 1 of
+// them, into m, l, s; several parts are in flight.
+template <int D, int V>
+__device__ __forceinline__ void join_parts(const Args &a, const Split &sp, int h, int d, int k0, int step, float &m, float &l,
+                                           float (&s)[V]) {
+    constexpr int kFlight = V == 1 ? 12 : 8;
+    m = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; i++) s[i] = 0.0f;
-    for (int k0 = w; k0 < sp.parts; k0 += kFlight * W) {
+    for (; k0 < sp.parts; k0 += kFlight * step) {
         float pm[kFlight], pl[kFlight], t[kFlight][V];
 #pragma unroll
         for (int j = 0; j < kFlight; j++) {
-            const int k = k0 + j * W;
+            const int k = k0 + j * step;
             pm[j] = -INFINITY, pl[j] = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; i++) t[j][i] = 0.0f;
@@ -637,30 +625,48 @@ attn_decode_join_kernel(const Args a, int64_t units) {
         }
         m = mn;
     }
-    if constexpr (W > 1) {
-        if (lane == 0) sm[warp] = m, sl[warp] = l;
+}
+
+// The same over the W warps of a CTA; the result is the first warp's.
+template <int D, int V, int W>
+__device__ __forceinline__ void join_cta(const Args &a, const Split &sp, int h, int d, float &m, float &l, float (&s)[V]) {
+    __shared__ float sm[W], sl[W], sums[W][32 * V];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    join_parts<D, V>(a, sp, h, d, warp, W, m, l, s);
+    if (lane == 0) sm[warp] = m, sl[warp] = l;
 #pragma unroll
-        for (int i = 0; i < V; i++) sums[warp][lane * V + i] = s[i];
-        __syncthreads();
-        if (warp > 0) return;
-        const float lm = lane < W ? sm[lane] : -INFINITY;
-        m = lm;
+    for (int i = 0; i < V; i++) sums[warp][lane * V + i] = s[i];
+    __syncthreads();
+    if (warp > 0) return;
+    const float lm = lane < W ? sm[lane] : -INFINITY;
+    m = lm;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float f = m == -INFINITY ? 0.0f : ex2(lm - m);
-        l = lane < W ? sl[lane] * f : 0.0f;
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float f = m == -INFINITY ? 0.0f : ex2(lm - m);
+    l = lane < W ? sl[lane] * f : 0.0f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
-        for (int i = 0; i < V; i++) s[i] = 0.0f;
+    for (int i = 0; i < V; i++) s[i] = 0.0f;
 #pragma unroll
-        for (int x = 0; x < W; x++) {
-            const float fx = __shfl_sync(0xffffffffu, f, x);
+    for (int x = 0; x < W; x++) {
+        const float fx = __shfl_sync(0xffffffffu, f, x);
 #pragma unroll
-            for (int i = 0; i < V; i++) s[i] = fmaf(sums[x][lane * V + i], fx, s[i]);
-        }
+        for (int i = 0; i < V; i++) s[i] = fmaf(sums[x][lane * V + i], fx, s[i]);
     }
-    const int64_t row = (int64_t)seq * a.q_heads + kvh * a.group + chunk * a.per_chunk + h;
+}
+
+// Output row of head h of unit u; -1 if it has no such head.  (A call whose units
+// pass 32 bits has more tiles than positions, and no parts.)
+__device__ __forceinline__ int64_t row_of_head(const Args &a, int64_t u, int h) {
+    const unsigned kv = (unsigned)u / (unsigned)a.chunks, chunk = (unsigned)u - kv * a.chunks;
+    const unsigned seq = kv / (unsigned)a.kv_heads, kvh = kv - seq * a.kv_heads;
+    if (h >= a.group - (int)chunk * a.per_chunk) return -1;
+    return (int64_t)seq * a.q_heads + (int)(kvh * a.group + chunk * a.per_chunk) + h;
+}
+// Its elements from d on, and its lse.
+template <int D, typename T, int V>
+__device__ __forceinline__ void finish_row(const Args &a, int64_t row, int d, float m, float l, float (&s)[V]) {
     T *out = static_cast<T *>(a.out) + row * D + d;
     float *lse = a.lse && d == 0 ? a.lse + row : nullptr;
     if constexpr (V == 1) {
@@ -669,6 +675,60 @@ attn_decode_join_kernel(const Args a, int64_t units) {
         if (lse) *lse = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     } else {
         finish<V>(out, lse, m, l, s);
+    }
+}
+
+// Joins a unit that lies in parts: W warps take head blockIdx.y of it, a lane
+// holding D / (32 Z) elements of slice blockIdx.z.
+template <int D, typename T, int W, int Z>
+__global__ void __launch_bounds__(32 * W)
+attn_decode_join_kernel(const Args a) {
+    constexpr int V = D / (32 * Z);
+    const int h = blockIdx.y, d = blockIdx.z * 32 * V + (threadIdx.x & 31) * V;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t u = blockIdx.x;
+    const Split sp = a.splits[u];
+    const int64_t row = row_of_head(a, u, h);
+    if (sp.parts < 2 || row < 0) return;
+    float m, l, s[V];
+    join_cta<D, V, W>(a, sp, h, d, m, l, s);
+    if (threadIdx.x < 32) finish_row<D, T, V>(a, row, d, m, l, s);
+}
+
+// The same for many units, a warp each.  How many parts a unit lies in is known
+// here only: one long sequence among many short ones can have nearly all of
+// them, and takes the CTA's warps together (131071 tokens and 299 sequences of 32,
+// one head: 154 us with a warp for each unit, 41 so; 100000 and 63 of 100, 8 heads: 88
+// and 70).  Neighbouring units, a sequence's heads, are in different CTAs.
+constexpr int kAlone = 16;  // parts that a warp joins by itself, in two rounds of loads
+template <int D, typename T>
+__global__ void __launch_bounds__(256)
+attn_decode_join_many_kernel(const Args a, int64_t units) {
+    constexpr int V = D / 32;
+    __shared__ Split split[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y, d = lane * V;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t u = (int64_t)warp * gridDim.x + blockIdx.x;
+    Split sp = {0, 0, 0, 0};
+    if (u < units) sp = a.splits[u];
+    const int64_t row = row_of_head(a, u, h);
+    if (row < 0) sp.parts = 0;
+    if (lane == 0) split[warp] = sp;
+    const bool any = __syncthreads_or(sp.parts > kAlone);
+    float m, l, s[V];
+    if (sp.parts >= 2 && sp.parts <= kAlone) {
+        join_parts<D, V>(a, sp, h, d, 0, 1, m, l, s);
+        finish_row<D, T, V>(a, row, d, m, l, s);
+    }
+    if (!any) return;
+    for (int i = 0; i < 8; i++) {
+        const Split one = split[i];
+        if (one.parts <= kAlone) continue;
+        join_cta<D, V, 8>(a, one, h, d, m, l, s);
+        if (warp == 0) finish_row<D, T, V>(a, row_of_head(a, (int64_t)i * gridDim.x + blockIdx.x, h), d, m, l, s);
+        __syncthreads();  // the first warp has read what the others left
     }
 }
 
@@ -736,18 +796,18 @@ cudaError_t launch(const Args &a, const bitnet_kv_cache &cache, int grid, cudaSt
     const int64_t units = (int64_t)a.seqs * a.kv_heads * a.chunks, warps = (int64_t)grid * kWarps;
     cfg.dynamicSmemBytes = 0;
     if (units * 4 >= warps || units * a.per_chunk > 8 * num_sms()) {
-        cfg.gridDim = dim3((unsigned)((units + 3) / 4), (unsigned)a.per_chunk);
-        cfg.blockDim = dim3(128);
-        return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, T, 1, 1>, a, units);
+        cfg.gridDim = dim3((unsigned)((units + 7) / 8), (unsigned)a.per_chunk);
+        cfg.blockDim = dim3(256);
+        return cudaLaunchKernelEx(&cfg, attn_decode_join_many_kernel<D, T>, a, units);
     }
     cfg.gridDim = dim3((unsigned)units, (unsigned)a.per_chunk);
     if (units * 100 >= warps) {
         cfg.blockDim = dim3(32 * 8);
-        return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, T, 8, 1>, a, units);
+        return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, T, 8, 1>, a);
     }
     cfg.gridDim.z = D / 32;
     cfg.blockDim = dim3(32 * 32);
-    return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, T, 32, D / 32>, a, units);
+    return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, T, 32, D / 32>, a);
 }
 
 template <int D>

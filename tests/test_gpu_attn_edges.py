@@ -368,3 +368,19 @@ def test_decode_wait_that_runs_out(dim, t, lens):
         assert b.bitnet_get_device_error() == b.BITNET_OK
         assert np.array_equal(got, want) and np.array_equal(lse, wl)
     check_cache(dev, cache, "after")
+
+
+@pytest.mark.parametrize("dim,t,hk,group,lens", [
+    (128, "f32", 1, 4, [20] * 296 + [30000, 3, 15000, 0, 9000]),   # long ones beside each other and alone
+    (128, "bf16", 2, 8, [17] * 100 + [20000] + [40] * 60),
+    (64, "f16", 1, 12, [25000] + [30] * 300),                      # two chunks of heads, the first unit long
+    (64, "f32", 4, 1, [0, 1] * 60 + [12000]),
+])
+def test_decode_a_long_sequence_among_many_short_ones(dim, t, hk, group, lens):
+    """A unit in hundreds of parts among hundreds that lie in one: right, and the same bits again."""
+    cache, table, q = decode_case(dim, t, 64, hk, group, lens, seed=71)
+    dev = dev_cache(cache)
+    got, lse = run_decode(dev, q, lens, table, t)
+    check_decode(cache, table, q, lens, t, got, lse)
+    again, l2 = run_decode(dev, q, lens, table, t)
+    assert np.array_equal(got, again) and np.array_equal(lse, l2)
