@@ -51,7 +51,7 @@
 #include <type_traits>
 
 #include "attn.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_f16.cuh"
 
 namespace bitnet {
 namespace {

@@ -286,3 +286,15 @@ def test_prompt_exponential_polynomial_up_to_the_largest_weight():
     got = np.ldexp(p.astype(np.float64), n.astype(int))
     assert np.abs(got / np.exp2(y.astype(np.float64)) - 1.0).max() <= 2.0 ** -18.4 + 5 * 1.5 * 2.0 ** -24
     assert got.max() < 65504
+
+
+def test_traffic_records_belong_to_the_sources():
+    """A capture counts only for the sources that it was made of: what other kernels need stays out of their headers,
+    or the capture is made again."""
+    import json
+    import sys
+    sys.path.insert(0, ROOT)
+    import bench
+    for kernel, d in json.load(open(os.path.join(ROOT, "profiles", "traffic.json"))).items():
+        traffic, note = bench.read_traffic(kernel, d["algorithmic_bytes"])
+        assert traffic == d["dram_bytes"], f"{kernel}: {note}"
