@@ -1,8 +1,25 @@
 // abi_attn.cu -- the entry points of the cache and attention calls: host-side
 // validation, then one launch.  Declarations: include/bitnet_w2a8.h.
+#include <atomic>
+
 #include "attn.cuh"
 
 namespace bitnet {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode() {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult q;
+        void *p = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        fn.store(f, std::memory_order_release);
+    }
+    return f;
+}
+
 namespace {
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }

@@ -4,12 +4,15 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cudaTypedefs.h>
 
 #include "common.cuh"
 
 namespace bitnet {
 
 constexpr int kKvBlock = BITNET_KV_BLOCK;
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode();  // NULL if the driver has none
 
 cudaError_t launch_kv_append(const bitnet_kv_cache &c, const bitnet_kv_append_args &a, const DeviceGlobals &g,
                              cudaStream_t st);
@@ -34,6 +37,11 @@ cudaError_t launch_attn_decode(const DecodeCall &d, const DeviceGlobals &g, cuda
 cudaError_t launch_attn_prompt(const bitnet_attn_prompt_args &a, const DeviceGlobals &g, cudaStream_t st);
 
 #ifdef __CUDACC__
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // The larger; NaN where an operand is (fmaxf gives the other operand).
 __device__ __forceinline__ float max_nan(float a, float b) {
     float y;

@@ -43,7 +43,6 @@
 // shared memory at the end of each unit, lost 10 to 40 % of a batch in those
 // joins; joining the parts in the last CTA to arrive at a counter cost 6.7 us of a
 // 13.7 us call, fences and the atomic being dearer than a dependent launch.)
-#include <cudaTypedefs.h>
 
 #include <atomic>
 #include <type_traits>
@@ -119,11 +118,6 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t r;
@@ -732,23 +726,9 @@ attn_decode_join_many_kernel(const Args a, int64_t units) {
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
-    PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
-    if (!f) {
-        cudaDriverEntryPointQueryResult q;
-        void *p = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-        fn.store(f, std::memory_order_release);
-    }
-    return f;
-}
-
 // The cache's codes as rows of head_dim bytes, boxes of a tile's rows in one page.
 bool make_map(CUtensorMap *m, const int8_t *codes, const bitnet_kv_cache &c) {
-    auto enc = encode_fn();
+    auto enc = tensor_map_encode();
     if (!enc) return false;
     cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.num_pages * c.kv_heads * c.page_size};
     cuuint64_t strides[1] = {(cuuint64_t)c.head_dim};

@@ -43,9 +43,7 @@
 //
 // Every wait is bounded; a CTA whose wait ran out latches the error word, ends
 // its copies and MMAs (bounded) and frees its tensor memory.
-#include <cudaTypedefs.h>
 #include <limits.h>
-#include <string.h>
 
 #include <atomic>
 #include <type_traits>
@@ -116,12 +114,6 @@ struct Cfg {
     static __device__ __forceinline__ uint32_t s_at(int s) { return (uint32_t)(kKeys * s); }
     static __device__ __forceinline__ uint32_t o_at(int s) { return (uint32_t)(kSlots * kKeys + D * s); }
 };
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // NaN where an operand is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -658,24 +650,10 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, C::kTmemCols);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
-    PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
-    if (!f) {
-        cudaDriverEntryPointQueryResult q;
-        void *p = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-        fn.store(f, std::memory_order_release);
-    }
-    return f;
-}
-
 // [tokens][heads][dim] rows of `stride` elements, boxes of `rows` tokens x 64
 // elements of one head; rows behind the last token read as 0.
 bool make_map(CUtensorMap *m, const void *p, bool bf16, int dim, int heads, int64_t tokens, int64_t stride, int rows) {
-    auto enc = encode_fn();
+    auto enc = tensor_map_encode();
     if (!enc) return false;
     if (tokens == 1 && stride < (int64_t)heads * dim) stride = (int64_t)heads * dim;  // one row: no stride is used
     cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
