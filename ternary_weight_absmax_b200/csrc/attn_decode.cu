@@ -275,9 +275,11 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     for (int i = 0; i < kStages - 1; i++) sc[i] = 1.0f;
 
     // The page of a block: read a tile before it is used, so that no check
-    // waits for it here.
+    // waits for it here.  (An ordinary load, as that of the scales: the non-coherent path
+    // is for memory that no one writes while the kernel runs, and this one starts
+    // beside the append.)
     auto page_of = [&](int blk) -> int {
-        return (int64_t)blk * kKvBlock < len ? __ldg(table + (blk << 4 >> a.page_shift)) : 0;
+        return (int64_t)blk * kKvBlock < len ? table[blk << 4 >> a.page_shift] : 0;
     };
     auto pages_of = [&](int t) {
         page0 = page_of(2 * t);
@@ -313,7 +315,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         tile_no++;
         const int r = lane & 2 ? r1 : r0;
         const bool have = r >= 0 && (2 * t + (lane >> 1 & 1)) * kKvBlock < len;
-        if (lane < 4 && have) scale = __ldg((lane & 1 ? a.vs : a.ks) + (r >> 4));
+        if (lane < 4 && have) scale = (lane & 1 ? a.vs : a.ks)[r >> 4];
     };
     // Moves on to the unit that `at` lies in, and asks for its first tiles.
     auto begin_unit = [&]() {

@@ -298,3 +298,13 @@ def test_traffic_records_belong_to_the_sources():
     for kernel, d in json.load(open(os.path.join(ROOT, "profiles", "traffic.json"))).items():
         traffic, note = bench.read_traffic(kernel, d["algorithmic_bytes"])
         assert traffic == d["dram_bytes"], f"{kernel}: {note}"
+
+
+def test_no_non_coherent_loads_beside_the_append():
+    """The cache and attention kernels start while the kernel before them still writes (dependent launch); what they read
+    after their wait may not go through the path for memory that is constant as long as a kernel runs."""
+    import re
+    csrc = os.path.join(ROOT, "ternary_weight_absmax_b200", "csrc")
+    for n in ("attn.cuh", "attn_decode.cu", "attn_prompt.cu", "kv_cache.cu"):
+        src = open(os.path.join(csrc, n)).read()
+        assert not re.search(r"__ldg\b|ld\.global\.nc|const\s+\w+\s*\*\s*__restrict__", src), n
