@@ -308,3 +308,34 @@ def test_no_non_coherent_loads_beside_the_append():
     for n in ("attn.cuh", "attn_decode.cu", "attn_prompt.cu", "kv_cache.cu"):
         src = open(os.path.join(csrc, n)).read()
         assert not re.search(r"__ldg\b|ld\.global\.nc|const\s+\w+\s*\*\s*__restrict__", src), n
+
+
+@pytest.mark.parametrize("dim,keys,stages", [(64, 64, 6), (128, 128, 4)])
+def test_prompt_guarded_tiles_fit_their_barriers(dim, keys, stages):
+    """The prompt kernel's count of tiles that a row sees in part, and how far two slots' walks are apart, over the
+    shapes that can differ: the bounds that its barriers and a phase rely on."""
+    import re
+    src = open(os.path.join(ROOT, "ternary_weight_absmax_b200", "csrc", "attn_prompt.cu")).read()
+    most_guarded = int(re.search(r"kGuarded = (\d+);", src).group(1))
+    rng = np.random.default_rng(1)
+    worst = 0
+    for _ in range(60000):
+        lq, lk, group = (int(x) for x in (rng.integers(1, 700), rng.integers(0, 900), rng.integers(1, 4)))
+        causal = bool(rng.integers(0, 4))
+        items = -(-lq // 128) * group
+        pair = int(rng.integers(0, (items + 1) // 2))
+        shift, row0, tiles = lk - lq, [], []
+        for item in (2 * pair, 2 * pair + 1):
+            r = item // group * 128
+            seen = min(lk, min(r + 128, lq) + shift) if causal else lk
+            tiles.append(-(-seen // keys) if item < items and seen > 0 else 0)
+            row0.append(r)
+        guard0 = max(0, min(lk, row0[0] + shift + 1) if causal else lk) // keys
+        worst = max(worst, max(tiles) - guard0)
+        for s in range(2):
+            if tiles[s]:
+                assert max(tiles) - tiles[s] < stages // 2
+                last = min(lq, row0[s] + 128)
+                for r in (row0[s], last - 1):   # before guard0 every row sees the whole tile
+                    assert guard0 * keys <= max(0, min(lk, r + shift + 1) if causal else lk)
+    assert worst <= most_guarded

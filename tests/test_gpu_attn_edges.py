@@ -384,3 +384,50 @@ def test_decode_a_long_sequence_among_many_short_ones(dim, t, hk, group, lens):
     check_decode(cache, table, q, lens, t, got, lse)
     again, l2 = run_decode(dev, q, lens, table, t)
     assert np.array_equal(got, again) and np.array_equal(lse, l2)
+
+
+def test_captured_prompt_calls_serve_any_bounds():
+    """Append, gather and prompt attention in one graph whose bounds and lengths are changed on the device between the
+    replays: the bits of the same calls made directly, rows behind the last sequence left as they were."""
+    b, tt = lib(), torch()
+    rng = np.random.default_rng(81)
+    dim, hk, group, page, seqs, rows = 128, 2, 2, 32, 3, 400
+    hq = hk * group
+    table = cuda(np.arange(seqs * 16, dtype=np.int32).reshape(seqs, 16))
+    qkv = cuda(rng.normal(0, 1, (rows, (hq + 2 * hk) * dim)).astype(np.float32))
+    rope = cuda(ref.angles(600, dim))
+    cu, old, cu_k = ints(0, 0, 0, 0), ints(0, 0, 0), ints(0, 0, 0, 0)
+
+    def state():
+        dev = dev_cache(ref.Cache(seqs * 16, hk, page, dim))
+        return dev, tt.zeros((rows, hq, dim), device="cuda").half(), \
+            [tt.zeros((2 * rows, hk, dim), device="cuda").half() for _ in range(2)], tt.zeros((rows, hq, dim), device="cuda")
+
+    def calls(dev, q16, kv, out):
+        b.bitnet_kv_append(dev, *split(qkv, hq, hk, dim), cu, old, table, q16, rope=rope)
+        b.bitnet_kv_gather(dev, cu_k, table, *kv)
+        b.bitnet_attn_prompt(q16, *kv, cu, cu_k, out)
+
+    direct, captured = state(), state()
+    side, graph = tt.cuda.Stream(), tt.cuda.CUDAGraph()
+    side.wait_stream(tt.cuda.current_stream())
+    with tt.cuda.graph(graph, stream=side):
+        calls(*captured)
+    tt.cuda.current_stream().wait_stream(side)
+    lengths = np.zeros(seqs, np.int32)
+    for new in ([100, 1, 150], [0, 250, 17], [1, 1, 1], [130, 0, 0]):
+        cu.copy_(cuda(cu_of(new)))
+        old.copy_(cuda(lengths))
+        lengths = lengths + np.array(new, np.int32)
+        cu_k.copy_(cuda(cu_of(lengths)))
+        for st in (direct, captured):
+            st[3].fill_(9.0)
+        calls(*direct)
+        graph.replay()
+        tt.cuda.synchronize()
+        assert b.bitnet_get_device_error() == b.BITNET_OK
+        for n in ("k", "v", "k_scale", "v_scale"):
+            assert tt.equal(getattr(direct[0], n), getattr(captured[0], n)), n
+        for x, y in zip((direct[1], *direct[2], direct[3]), (captured[1], *captured[2], captured[3])):
+            assert tt.equal(x, y)
+        assert bool((captured[3][sum(new):] == 9).all()) and bool(tt.isfinite(captured[3]).all())
