@@ -188,7 +188,6 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    unsigned char *gbase = smem_raw + (base - raw);
     const uint32_t bars = base + C::kOffBar;
     auto q_full = [&](int s) { return bars + 8u * s; };
     auto s_full = [&](int s) { return bars + 8u * (2 + s); };
@@ -200,10 +199,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     auto v_land = [&](int g) { return kv_full(2 * kStages + g); };
     const uint32_t drain = kv_full(2 * kStages + kGuarded);
     static_assert((6 + kSlots * kParts + 2 * kStages + kGuarded + 1) * 8 + 12 <= C::kOffFirst - C::kOffBar, "barriers");
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + (drain + 8u - base));
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    volatile int *not_finite = abort_flag + 1;
-    int *first_at = reinterpret_cast<int *>(gbase + C::kOffFirst);
+    const uint32_t tmem_slot = drain + 8u, abort_flag = drain + 12u, not_finite = drain + 16u;  // words
+    auto first_at = [&](int kind, int d) { return base + C::kOffFirst + 4u * (kind * D + d); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // What needs no memory of an earlier kernel comes before the wait for it.
@@ -220,7 +217,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         }
         for (int g = 0; g < kGuarded; g++) ptx::mbar_init(v_land(g), 1);
         ptx::mbar_init(drain, 1);
-        *abort_flag = *not_finite = 0;
+        ptx::sts_flag(abort_flag, 0);
+        ptx::sts_flag(not_finite, 0);
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&map_q);
         ptx::prefetch_tmap(&map_k);
@@ -265,20 +263,20 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const int most = max(tiles[0], tiles[1]);
     // Tiles before it are seen whole by every row of the slots.
     const int guard0 = max(0, a.causal ? min(lk, row0[0] + shift + 1) : lk) / kKeys;
-    for (int i = threadIdx.x; i < 3 * D; i += kThreads) first_at[i] = INT_MAX;
+    for (int i = threadIdx.x; i < 3 * D; i += kThreads) ptx::sts_flag(first_at(0, i), INT_MAX);
     const uint32_t limit = *a.wait_limit;
 
     if (warp == kMmaWarp) {
-        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::kTmemCols);
+        ptx::tmem_alloc(tmem_slot, C::kTmemCols);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = ptx::lds_flag(tmem_slot);
 
     auto give_up = [&]() {
-        *abort_flag = 1;
+        ptx::sts_flag(abort_flag, 1);
         atomicOr(a.err, kErrTimeout);
     };
     auto kv_at = [&](int t) { return base + C::kOffKv + (uint32_t)(t % kStages) * C::kTileBytes; };
@@ -298,7 +296,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             bool ok = true;
             for (int t = 0; t < 2 * most && ok; t++) {
                 if (t == 0 && tiles[0]) load(base, &map_q, q_full(0), head[0], q0 + row0[0], C::kQPiece);
-                if (t >= kStages && !ptx::mbar_wait(kv_empty(t % kStages), (t / kStages - 1) & 1, limit, abort_flag)) {
+                if (t >= kStages && !ptx::mbar_wait_flag(kv_empty(t % kStages), (t / kStages - 1) & 1, limit, abort_flag)) {
                     give_up();
                     ok = false;
                     break;
@@ -338,7 +336,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             const int n0 = tiles[0], n1 = tiles[1];
             bool ok = true;
             auto wait = [&](bool tried, uint32_t bar, uint32_t parity) {
-                if (!tried && ok && !ptx::mbar_wait(bar, parity, limit, abort_flag)) {
+                if (!tried && ok && !ptx::mbar_wait_flag(bar, parity, limit, abort_flag)) {
                     give_up();
                     ok = false;
                 }
@@ -417,7 +415,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const int first_masked = (a.causal ? min(lk, r0 + shift + 1) : lk) / kKeys;  // tiles before it need no mask
         bool ok = true;
         for (int j = 0; j < n; j++) {
-            if (!ptx::mbar_wait(s_full(s), j & 1, limit, abort_flag)) {
+            if (!ptx::mbar_wait_flag(s_full(s), j & 1, limit, abort_flag)) {
                 give_up();
                 ok = false;
             }
@@ -544,8 +542,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             // rows, less than the ring holds: its stage has not gone on).
             static_assert(kTile / kKeys < kStages / 2, "phase of the last V");
             const int tv = 2 * n - 1;
-            hurt = ptx::mbar_wait(kv_full(tv % kStages), tv / kStages & 1, limit, abort_flag) && *not_finite;
-            if (!ptx::mbar_wait(o_full(s), 0, limit, abort_flag)) {
+            hurt = ptx::mbar_wait_flag(kv_full(tv % kStages), tv / kStages & 1, limit, abort_flag) && ptx::lds_flag(not_finite);
+            if (!ptx::mbar_wait_flag(o_full(s), 0, limit, abort_flag)) {
                 give_up();
                 ok = false;
             }
@@ -574,9 +572,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 #pragma unroll 1
                 for (int d = 0; d < D; d++) {
                     float x = (float)dst[d];
-                    if (first_at[d] < limit_col) x = NAN;
-                    if (first_at[D + d] < limit_col) x += INFINITY;
-                    if (first_at[2 * D + d] < limit_col) x -= INFINITY;
+                    if (ptx::lds_flag(first_at(0, d)) < limit_col) x = NAN;
+                    if (ptx::lds_flag(first_at(1, d)) < limit_col) x += INFINITY;
+                    if (ptx::lds_flag(first_at(2, d)) < limit_col) x -= INFINITY;
                     dst[d] = (Out)x;
                 }
             }
@@ -595,14 +593,15 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         constexpr uint32_t kInf = kBf16 ? 0x7f80u : 0x7c00u;
         const int me = (warp - kGuardWarp) * 32 + lane;
         for (int g = 0; g < most - guard0; g++) {
-            bool ok = ptx::mbar_wait(v_land(g), 0, limit, abort_flag);
+            bool ok = ptx::mbar_wait_flag(v_land(g), 0, limit, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
                 if (lane == 0) give_up();
                 break;
             }
             const int key0 = (guard0 + g) * kKeys, keys = lk - key0;  // from this tile on
-            uint4 *v = reinterpret_cast<uint4 *>(gbase + (kv_at(2 * (guard0 + g) + 1) - base));
+            unsigned char *const smem = smem_raw + (base - raw);
+            uint4 *v = reinterpret_cast<uint4 *>(smem + (kv_at(2 * (guard0 + g) + 1) - base));
             // 16-byte chunk e of a piece is number e & 7 (swizzled) of row e / 8.
             const int own = min(keys, kKeys) * 8;
             P2 sum[4];  // of 0 times the values: NaN if one is not finite
@@ -632,11 +631,11 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     for (int i = 0; i < 8; i++) {
                         if ((x[i] & kInf) != kInf) continue;
                         const int kind = (x[i] & 0x7fffu) != kInf ? 0 : x[i] == kInf ? 1 : 2;
-                        atomicMin(first_at + kind * D + column + i, key0 + row);
+                        atomicMin(reinterpret_cast<int *>(smem + (first_at(kind, column + i) - base)), key0 + row);
                         x[i] = 0;
                     }
                 }
-                if (lane == 0) *not_finite = 1;
+                if (lane == 0) ptx::sts_flag(not_finite, 1);
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();

@@ -9,6 +9,25 @@
 namespace bitnet {
 namespace ptx {
 
+// Flags in shared memory by their 32-bit address (a pointer that lives across the
+// softmax of a row takes two of its registers).
+__device__ __forceinline__ int lds_flag(uint32_t addr) {
+    int v;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts_flag(uint32_t addr, int v) {
+    asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// mbar_wait, giving up early once the flag at `abort` is set.
+__device__ __forceinline__ bool mbar_wait_flag(uint32_t bar, uint32_t parity, uint32_t limit, uint32_t abort) {
+    for (uint32_t i = 0; i < limit; i++) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (lds_flag(abort)) return false;
+    }
+    return false;
+}
+
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
