@@ -415,8 +415,9 @@ typedef enum {
 /* The cache, caller owned.  Page p, head h, slot r (0 .. page_size-1):
  *   codes   k, v              int8 [num_pages][kv_heads][page_size][head_dim]
  *   scales  k_scale, v_scale  fp32 [num_pages][kv_heads][page_size / 16]
- * a value is code / scale.  Token t of a sequence is in slot t % page_size of
- * page block_table[seq][t / page_size].  The memory needs no initial value.
+ * a value is code / scale (bitnet_kv_gather: code * (1 / scale)).  Token t of a
+ * sequence is in slot t % page_size of page block_table[seq][t / page_size].  The
+ * memory needs no initial value.
  * head_dim: 64 or 128.  page_size: a power of two, 16 .. 1024.  kv_heads:
  * 1 .. 1024.  num_pages * kv_heads * page_size: below 2^31 (137 GB of keys).
  * Codes 16-byte, scales 4-byte aligned. */
@@ -499,7 +500,9 @@ bitnet_status bitnet_kv_gather(const bitnet_kv_cache *cache, const int32_t *cu_t
  * t < seq_len[i] (the appended token included), group = q_heads / kv_heads.
  * Softmax and sums are held in fp32.  q enters the products as 24-bit integers
  * relative to the largest element of its head (BF16 calls: 16-bit), the softmax
- * weights as two fp16 parts (BF16: one), codes as themselves.  q rows of
+ * weights as two fp16 parts (BF16: one), codes as themselves; the sum of weights
+ * (at most 1) times values is fp32 before it is divided, and may pass to infinity
+ * where values exceed 3e38 / tokens.  q rows of
  * q_stride elements, out contiguous [seqs][q_heads][dim], both of `dtype`; lse
  * (nullable) fp32 [seqs][q_heads] receives the natural logarithm of the sum of
  * exponentials.  No tokens: out is 0, lse -inf; a head of q that holds a NaN or
@@ -545,12 +548,15 @@ typedef struct {
  * / 1.443 on) is NaN, its lse as well; a score of -inf is a key without weight.
  * Keys and values that a row does not see may be anything, NaN and infinities
  * included; where a row sees a value that is NaN or infinite, that element of its
- * output is not finite.  (F16: a weight below 2^-21 of the largest so far is held
- * to 2^-32 of it.)  Scores, softmax and sums are fp32; the softmax weights are rounded
- * once to dtype, as operands of the second product (neighbouring rows of a
+ * output is not finite.  Scores, softmax and sums are fp32; the softmax weights
+ * are rounded once to dtype, as operands of the second product (F16: one below
+ * 2^-21 of the largest so far is held to 2^-32 of it).  Neighbouring rows of a
  * sequence share when a running maximum moves, so they may change a row's last
- * bits, never more; other sequences change nothing).  out and lse may not overlap inputs.  Rows behind the last sequence are not written.  head_dim 64 or 128; rows 16-byte aligned, strides
- * multiples of 8.
+ * bits, never more; other sequences change nothing.  The sum of weights times
+ * values is fp32 before it is divided, a weight at most 2^8 (BF16): it may pass to
+ * infinity where values exceed 1e36 / keys.  out and lse may not overlap inputs.
+ * Rows behind the last sequence are not written.  head_dim 64 or 128; rows 16-byte
+ * aligned, strides multiples of 8.
  * Errors: NULL, SHAPE, ALIGN, VALUE, UNSUPPORTED (not an sm_100 device), CUDA;
  * bounded device waits that run out latch BITNET_ERR_TIMEOUT. */
 bitnet_status bitnet_attn_prompt(const bitnet_attn_prompt_args *args, bitnet_stream_t stream);
@@ -561,7 +567,9 @@ bitnet_status bitnet_attn_prompt(const bitnet_attn_prompt_args *args, bitnet_str
 
 /* Waits for `stream`, then reads and clears the current device's error word:
  * BITNET_OK, BITNET_ERR_TIMEOUT (a bounded wait ran out), BITNET_ERR_CORRUPT
- * (a kernel met code 3) or BITNET_ERR_CUDA (the stream itself failed). */
+ * (a kernel met code 3), BITNET_ERR_VALUE (a page, length, position or bound that
+ * the cache and attention calls do not follow) or BITNET_ERR_CUDA (the stream
+ * itself failed). */
 bitnet_status bitnet_get_device_error(bitnet_stream_t stream);
 
 /* Test hook: sets the iteration cap of the device-side bounded waits on the

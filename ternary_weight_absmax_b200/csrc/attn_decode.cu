@@ -1,16 +1,18 @@
 // attn_decode.cu -- attention of one token per sequence over the paged int8
 // cache:  out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q.k_t - max).
 //
-// Bound: the cache is read once from HBM (2 D bytes a token and kv head); all
-// query heads of a kv head are served from the one read.  Measured, heads of 128:
-// 64 x 4k, 8 kv heads, fp32 104 us (4.6 TB/s); 8 x 32k, bf16 96 us (5.5 TB/s);
-// 1 x 131071, 5 kv heads, bf16 40 us, 9 of them start and join; 1 x 700 9 us.  Short
-// sequences are bound by latency (256 x 500, 2 kv heads of 64: 25 us, 1.3 TB/s).
+// Bound: the cache is read from HBM (2 D bytes a token and kv head), once for up to
+// 8 query heads of a kv head; larger groups go through it once for each 8 (the
+// second time mostly from L2: 64 x 4k, 16 query heads on each of 2 kv heads, 58 us).
+// Measured, heads of 128: 64 x 4k, 32 on 8 heads, fp32 104 us (4.6 TB/s), bf16 96;
+// 8 x 32k, bf16 96 us (5.5 TB/s); 1 x 131071, 5 kv heads, bf16 40 us, 9 of them start
+// and join; 1 x 700 8.6 us.  Short sequences are bound by latency (256 x 500, 2 kv
+// heads of 64: 25 us, 1.3 TB/s).
 //
 // Products, on the warp-level MMAs, transposed so that tokens (scores) and
-// elements (output) are the 16 rows and up to 8 query heads the 8 columns: no
-// row or column idles at 8 heads a kv head, and the output of a head takes half
-// the registers that heads as rows would.
+// elements (output) are the 16 rows and up to 8 query heads the 8 columns: the
+// output of a head takes half the registers that heads as rows would.  At 8 heads a
+// kv head no row or column idles; at 4 half of the columns do.
 //   Scores (m16n8k32, int8, exact int32 sums): codes are operands as they are.
 //   A query is v m / 8355000 with m its head's largest element and v a 24-bit
 //   integer, split into three signed bytes (bf16 calls: 16 bits, two bytes), an
@@ -770,11 +772,12 @@ cudaError_t launch(const Args &a, const bitnet_kv_cache &cache, int grid, cudaSt
     e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, T>, mk, mv, a);
     if (e != cudaSuccess) return e;
     // On average a unit has warps / units parts and one more: up to five are one
-    // warp's, up to about 100 a CTA's of eight (32 x 750, 5 kv heads, seven parts:
-    // 21.4 us, with a warp's 22.2); beyond, a CTA of 32 warps takes a slice of 32
-    // elements.  More CTAs of eight warps than the SMs hold at once cost more than
-    // the parts: those units are a warp's too (150 x 250, heads of 64, 2 kv heads of
-    // 8 heads: 17.5 -> 13.4 us; 100 x 1500: 25.0 -> 22.7).
+    // warp's, up to about 100 a CTA's of eight (32 x 750, 5 kv heads, seven parts: 15.2
+    // us either way; 8 x 32k, 64 units: 95 us, with a warp's 111); beyond, a CTA of 32
+    // warps takes a slice of 32 elements (1 x 700: 8.7 us, with a warp's 14.6).  More
+    // CTAs of eight warps than the SMs hold at once cost more than the parts: those
+    // units are a warp's too (150 x 250, heads of 64, 2 kv heads of 8 heads: 15.8 ->
+    // 11.1 us; 100 x 1500: 22.0 -> 20.0; 64 x 4k, 16 on each of 2 heads of 128: 61.9 -> 58.2).
     const int64_t units = (int64_t)a.seqs * a.kv_heads * a.chunks, warps = (int64_t)grid * kWarps;
     cfg.dynamicSmemBytes = 0;
     if (units * 4 >= warps || units * a.per_chunk > 8 * num_sms()) {

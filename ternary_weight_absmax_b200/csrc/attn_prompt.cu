@@ -36,10 +36,12 @@
 //
 // Bound: the tensor cores' 4 D operations a score at D = 128, the softmax (a
 // special function unit's exponential and about four instructions a score) at
-// D = 64.  Causal, 32 heads on 8 kv heads, 8192 tokens, bf16: 447 us, 1229 TFLOP/s
-// in a burst; heads of 64 (fp16): 348 us, 789 TFLOP/s.  Prompts of a few hundred
-// tokens (16 x 512, heads of 64: 35 us) are a CTA's start, end and the imbalance
-// of a few tiles.
+// D = 64.  Causal, 32 heads on 8 kv heads, 8192 tokens, bf16: 426-440 us in a burst
+// (1250-1290 TFLOP/s), 505-530 in calls one after another, whose clock the power
+// limit lowers (1040-1090); heads of 64 (fp16): 388 us, 705 TFLOP/s.  Prompts of a few
+// hundred tokens (16 x 512, the same heads of 64: 66 us) are a CTA's start, end and the
+// imbalance of a few tiles.  The softmax's registers spill a little (ptxas: 12 bytes
+// stored at heads of 128, 20 to 36 at 64).
 //
 // Every wait is bounded; a CTA whose wait ran out latches the error word, ends
 // its copies and MMAs (bounded) and frees its tensor memory.
@@ -585,9 +587,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     } else if (warp >= kGuardWarp) {
         // ------------------------------------------------ V of the guarded tiles
         // Bound: the softmax beside it, whose time it mostly fits in.  3 prompts of up to 150
-        // tokens take 9.7 us with it and 9.3 without, 8192 tokens the same; 16 ragged ones of
-        // heads of 64 take 73 and 69, as long when no tile is guarded: the code around
-        // is compiled otherwise.  (More loads at once in a lane: 9.6 us, but 451 us against 444 on 8192.)
+        // tokens take 9.6 us with it and 9.3 without, 8192 tokens the same; 16 ragged ones of
+        // heads of 64 take 71 and 69, as long when no tile is guarded: the code around
+        // is compiled otherwise.  (More loads at once in a lane: 451 us against 444 on 8192.)
         using P2 = typename Pair<T>::type;
         constexpr int kPieceChunks = C::kPiece / 16;
         constexpr uint32_t kInf = kBf16 ? 0x7f80u : 0x7c00u;

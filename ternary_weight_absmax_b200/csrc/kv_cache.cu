@@ -14,12 +14,15 @@
 // Blocks are found without a pass over the lengths: with few tokens a sequence
 // (below 32/15) by a unit for each token, otherwise by a unit for each 16 and two
 // for each sequence, whichever makes the smaller grid.  Bound: HBM at prompt
-// sizes (8k tokens of 32 + 2 x 8 heads of 128 from fp32, k and v in bf16 as well: 89
-// us, 4.4 TB/s; what is missing is latency between a block's loads and its barrier),
-// latency at one token a sequence (1: 2.9 us, 256: 5.7 us).
+// sizes (8k tokens of 32 + 2 x 8 heads of 128 from fp32, k and v in bf16 as well: 90
+// us, 4.3 TB/s; what is missing is latency: a block is looked up before its vectors are
+// asked for, and waits at its barrier),
+// latency at one token a sequence (1: 3.0 us, 256: 6.0 us; 4.9 and 11.4 where the
+// scales fall and the older codes of the blocks are rewritten, which is done by
+// one warp a head and not begun before the new scale is known).
 //
 // Gather.  64 tokens of one head per CTA, 16 codes a thread and load; bound: HBM
-// (64k tokens of 8 heads of 128 to bf16: 79.5 us, 5.4 TB/s).
+// (64k tokens of 8 heads of 128 to bf16: 78.2 us, 5.5 TB/s).
 #include <algorithm>
 
 #include "attn.cuh"
@@ -493,7 +496,7 @@ cudaError_t launch_kv_append(const bitnet_kv_cache &c, const bitnet_kv_append_ar
     const int64_t units = by_token ? p.tokens : blocks;
     // A decode batch has little to do for each head: as many heads to a CTA as
     // leave no more CTAs than four for each SM, which run at once (256 sequences of 8
-    // kv heads and 32 query heads, with norms: 4 heads a CTA 5.7 us, 3 heads and a
+    // kv heads and 32 query heads, with norms, no scale falling: 4 heads a CTA 5.7 us, 3 heads and a
     // second wave 8.2, 8 heads 6.7; one head a CTA and units of 16 tokens 22).
     const int per_unit = by_token ? (int)std::max((int64_t)1, std::min((int64_t)c.kv_heads, 4 * (int64_t)num_sms() / units))
                                   : (c.kv_heads + 1) / 2;  // CTAs
