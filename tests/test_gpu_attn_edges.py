@@ -431,3 +431,41 @@ def test_captured_prompt_calls_serve_any_bounds():
         for x, y in zip((direct[1], *direct[2], direct[3]), (captured[1], *captured[2], captured[3])):
             assert tt.equal(x, y)
         assert bool((captured[3][sum(new):] == 9).all()) and bool(tt.isfinite(captured[3]).all())
+
+
+def test_prompt_calls_side_by_side():
+    """Both head sizes and the three packed calls on two streams at once: the bits of the calls alone."""
+    b, tt = lib(), torch()
+    g = tt.Generator(device="cuda")
+    g.manual_seed(91)
+    calls, outs, want = [], [], []
+    for dim, dt, lens in ((64, tt.float16, [700, 1, 333]), (128, tt.bfloat16, [40, 900])):
+        n = sum(lens)
+        q = tt.randn((n, 4, dim), generator=g, device="cuda").to(dt)
+        k, v = (tt.randn((n, 2, dim), generator=g, device="cuda").to(dt) for _ in range(2))
+        cu, table = cuda(cu_of(lens)), tt.arange(len(lens) * 32, dtype=tt.int32, device="cuda").view(len(lens), 32)
+        dev, zero = dev_cache(ref.Cache(len(lens) * 32, 2, 32, dim)), ints(*[0] * len(lens))
+        out, rows, k16 = tt.empty_like(q), [tt.empty_like(k) for _ in range(2)], tt.empty_like(k)
+
+        def call(stream, q=q, k=k, v=v, cu=cu, table=table, dev=dev, zero=zero, out=out, rows=rows, k16=k16):
+            b.bitnet_kv_append(dev, None, k, v, cu, zero, table, None, k_out=k16, stream=stream)
+            b.bitnet_kv_gather(dev, cu, table, *rows, stream=stream)
+            b.bitnet_attn_prompt(q, *rows, cu, cu, out, stream=stream)
+
+        calls.append(call)
+        outs.append((out, *rows, dev.k, dev.v_scale))
+        call(None)
+        tt.cuda.synchronize()
+        want.append([x.clone() for x in outs[-1]])
+    streams = [tt.cuda.Stream() for _ in range(2)]
+    for x in outs:
+        x[0].zero_()
+    tt.cuda.synchronize()
+    for _ in range(20):
+        for call, stream in zip(calls, streams):
+            call(stream)
+    tt.cuda.synchronize()
+    assert b.bitnet_get_device_error() == b.BITNET_OK
+    for got, ref_ in zip(outs, want):
+        for x, y in zip(got, ref_):
+            assert tt.equal(x, y)
